@@ -14,7 +14,8 @@ LIB = os.path.join(HERE, "libfp4w4a16.so")
 PROBE_LIB = os.path.join(HERE, "libfp4probe.so")
 PROBE_SOURCES = ["probe.hip"]
 BUILD_DIR = os.path.join(HERE, "_build")
-SOURCES = ["api.hip", "layout.hip", "gemv.hip", "gemm.hip", "quantize.hip"]
+SOURCES = ["api.hip", "layout.hip", "gemv.hip", "gemm.hip", "quantize.hip",
+           "mx_quant.hip", "mx_gemv.hip", "mx_gemm.hip"]
 ARCH = os.environ.get("FP4_OFFLOAD_ARCH", "gfx950")
 
 FLAGS = [

@@ -300,6 +300,88 @@ int fp4_quantize_rocmfp4(int fmt, int64_t N, int64_t K, const float* w, const fl
  */
 int fp4_quantize_q4_0(int64_t N, int64_t K, const float* w, void* blocks, void* stream);
 
+/*
+ * MXFP4 with both operands in 4 bits (W4A4). MXFP4 (OCP Microscaling Formats specification, version
+ * 1.0) holds a block of 32 values along the contracted axis as E2M1 codes and one E8M0 byte s, which
+ * stands for 2^(s - 127); s = 255 makes the whole block NaN:
+ *
+ *     value = e2m1(code) * 2^(s - 127)
+ *     y[m][n] = sum_k A[m][k] * B[n][k]          (A, B in MXFP4; sums in FP32)
+ *
+ * An operand of R rows and depth K, in device memory: row r's codes are the 16 ceil(K / 32) bytes at
+ * q + r * ldq, byte j holding element 2j (bits 0-3) and 2j + 1 (bits 4-7); its scales are the ceil(K / 32)
+ * bytes at s + r * lds. That is the layout in which MXFP4 checkpoints hold their weights, so they need no
+ * repacking. ldq and q are multiples of 16, lds and s of 4. When K is not a multiple of 32 the last block's
+ * codes past K are zeros (in both operands; fp4_quantize_mxfp4 writes them so). Scale bytes of a row past its
+ * last block, up to the next multiple of 4, are readable and ignored. ldq, lds and K are at most 2^22.
+ *
+ * Dense tensors have a type, a row stride `ld` in elements (at least the row's length) and the alignment of
+ * their element type; 16-byte aligned rows are fastest for y.
+ * Outputs must not overlap any input or the workspace.
+ */
+enum {
+  FP4_TYPE_F32 = 1,
+  FP4_TYPE_BF16 = 2,
+  FP4_TYPE_F16 = 3
+};
+
+typedef struct fp4_mx {
+  void* q;       /* codes (device); written only by fp4_quantize_mxfp4 */
+  void* s;       /* E8M0 scales (device) */
+  int64_t ldq;   /* bytes from one row's codes to the next */
+  int64_t lds;   /* bytes from one row's scales to the next */
+} fp4_mx;
+
+/*
+ * x[M][K] (FP32, bf16 or FP16) -> MXFP4 along the rows (`rows`: M rows of depth K), along the columns
+ * (`cols`: the transposed operand, K rows of depth M), or both from one reading of x; the one not wanted
+ * is NULL. A product contracts the axis that was quantised: y = x w^T takes x and w along their rows, its
+ * gradients take them and the gradient of y along their columns.
+ * Per block, with a the largest magnitude: s = max(floor(log2 a) - 2 + 127, 0), each value divided by
+ * 2^(s - 127) and rounded to the nearest E2M1 value, halves to the even code, at most 6 in magnitude. A block
+ * that holds an infinity or a NaN gets s = 255 and zero codes. The sign of a value that rounds to zero is kept.
+ * Scale bytes of `rows` past a row's last block, up to the next multiple of 4, are written as zeros.
+ * M = 0 is a no-op. Errors: FP4_ERR_ARG (unknown type; null x, q or s; neither rows nor cols), FP4_ERR_SHAPE
+ * (M, K or a stride too small), FP4_ERR_UNSUPPORTED (K, a stride or, with cols, M too large), FP4_ERR_ALIGN, FP4_ERR_HIP.
+ */
+int fp4_quantize_mxfp4(int type, int64_t M, int64_t K, const void* x, int64_t ldx, const fp4_mx* rows,
+                       const fp4_mx* cols, void* stream);
+
+/*
+ * The values of an MXFP4 operand (M rows of depth K) as FP32 or bf16, both of which hold every value below
+ * 2^127 exactly. Errors as fp4_quantize_mxfp4; FP16 gives FP4_ERR_ARG.
+ */
+int fp4_dequant_mxfp4(int type, int64_t M, int64_t K, const fp4_mx* a, void* out, int64_t ldo, void* stream);
+
+/*
+ * y[M][N] = A B^T with A (M rows) and B (N rows) of depth K in MXFP4; y is FP32, bf16 or FP16 (rounded once,
+ * from the FP32 sum). M <= 64 streams B through a kernel that splits K inside the workgroup; larger M runs tiles
+ * on the scaled matrix instruction, with K in parts where y has few tiles: each part writes an FP32 plane of the
+ * workspace and a second kernel adds the planes in order. Deterministic. A partial sum past FP32's range
+ * is an infinity and stays one, or becomes NaN where two of opposite sign meet.
+ * workspace: device memory, 16-byte aligned, needing no initial contents, used only while the call's kernels run
+ * on `stream`; with fewer than w4a4_matmul_workspace_bytes() bytes (or NULL) K is not split. M = 0 is a no-op.
+ * Errors: FP4_ERR_ARG (unknown type, null pointer), FP4_ERR_SHAPE, FP4_ERR_UNSUPPORTED, FP4_ERR_ALIGN, FP4_ERR_HIP.
+ */
+int w4a4_matmul(int out_type, int64_t M, int64_t N, int64_t K, const fp4_mx* a, const fp4_mx* b, void* y,
+                int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes w4a4_matmul can use for this shape on the current device, or a negative status. */
+int64_t w4a4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/*
+ * y[M][N] = Q(x) B^T: dense activations x[M][K], quantised along their rows as fp4_quantize_mxfp4 does, times
+ * MXFP4 weights; the result equals fp4_quantize_mxfp4 followed by w4a4_matmul up to the order of the FP32 sums.
+ * For few rows one kernel does both; otherwise the quantised activations go through the workspace, which must
+ * then hold at least w4a4_linear_workspace_bytes() less the K parts' planes (FP4_ERR_ARG if it does not; pass the
+ * full size). Errors as fp4_quantize_mxfp4 and w4a4_matmul.
+ */
+int w4a4_linear(int x_type, int out_type, int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx,
+                const fp4_mx* b, void* y, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of w4a4_linear for this shape on the current device (0: it takes none), or a negative status. */
+int64_t w4a4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
 #ifdef __cplusplus
 }
 #endif
