@@ -2,9 +2,10 @@
 
 Argument marshalling only: every function below checks tensor devices, dtypes and sizes,
 passes raw device pointers and the current HIP stream to the C entry point of the same
-name in libfp4w4a16.so, and raises RuntimeError on a negative status. All computation
-runs in the library's HIP kernels; there is no fallback path. Importing this package
-without the built library fails loudly.
+name in libfp4w4a16.so, and raises RuntimeError on a negative status (the MXFP4 operators
+do so in _fp4bind.so, the binding's native half). All computation runs in the library's HIP
+kernels; there is no fallback path. Importing this package without the built libraries fails
+loudly.
 """
 from __future__ import annotations
 
@@ -90,6 +91,8 @@ def lib() -> ctypes.CDLL:
 
 
 lib()  # fail at import time when the HIP library is absent
+
+from . import _fp4bind as _native  # noqa: E402  (links libfp4w4a16.so, loaded above)
 
 
 def _fmt(fmt) -> int:
@@ -404,77 +407,20 @@ class PackedWeight:
 # MXFP4 on both sides (W4A4): quantisation, products, a trainable linear layer
 # ----------------------------------------------------------------------------------------------
 
-DENSE_TYPES = {torch.float32: 1, torch.bfloat16: 2, torch.float16: 3}
-MX_BLOCK = 32
-
-
-def _dense_type(t: torch.Tensor, what: str, allowed=DENSE_TYPES) -> int:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what}: expected a torch.Tensor")
-    if t.dtype not in allowed:
-        raise TypeError(f"{what} must be one of {sorted(str(d) for d in allowed)}, not {t.dtype}")
-    return allowed[t.dtype]
-
-
-def _rows_of(t: torch.Tensor, rows: int, cols: int, what: str) -> int:
-    """Row stride (in elements) of a [rows, cols] matrix whose rows are contiguous."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError(f"{what} must have shape [{rows}, {cols}], not {list(t.shape)}")
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{what}: the elements of a row must be contiguous")
-    if rows > 1 and t.stride(0) < cols:
-        raise ValueError(f"{what}: rows overlap")
-    return t.stride(0) if rows > 1 else max(cols, 1)
-
-
-def _blocks(k: int) -> int:
-    return (k + MX_BLOCK - 1) // MX_BLOCK
-
-
-def _mx_struct(q, s, rows: int, k: int, what: str) -> Mx:
-    """The C operand of codes q [rows, 16 ceil(k / 32)] and scales s [rows, ceil(k / 32)] (uint8; row strides free)."""
-    nb = _blocks(k)
-    if q.dtype != torch.uint8 or s.dtype != torch.uint8:
-        raise TypeError(f"{what}: codes and scales must be uint8")
-    ldq = _rows_of(q, rows, 16 * nb, f"{what} codes")
-    lds = _rows_of(s, rows, nb, f"{what} scales")
-    if rows == 1:
-        lds = (nb + 3) // 4 * 4
-    # scale rows are read in whole dwords
-    end = s.storage_offset() + (rows - 1) * lds + (nb + 3) // 4 * 4
-    if rows > 0 and end > s.untyped_storage().nbytes():
-        raise ValueError(f"{what} scales: the last row must be readable up to a multiple of 4 bytes")
-    return Mx(q.data_ptr(), s.data_ptr(), ldq, lds)
-
-
 def fp4_quantize_mxfp4(M, K, x, q=None, s=None, qt=None, st=None, stream=None):
     """x [M, K] (float32, bfloat16 or float16; rows may be strided) -> MXFP4 along its rows into q [M, 16 ceil(K/32)] and
     s [M, ceil(K/32)], and / or along its columns into qt [K, 16 ceil(M/32)] and st [K, ceil(M/32)] (the transposed
     operand). One of the two pairs may be None. Rows of the scales lie a multiple of 4 bytes apart."""
-    ty = _dense_type(x, "x")
-    ldx = _rows_of(x, M, K, "x")
-    if (q is None) != (s is None) or (qt is None) != (st is None):
-        raise ValueError("codes and scales come in pairs")
-    dev = _device(x, q, s, qt, st)
-    rows = _mx_struct(q, s, M, K, "rows") if q is not None else None
-    cols = _mx_struct(qt, st, K, M, "columns") if qt is not None else None
-    with torch.cuda.device(dev):
-        _check(lib().fp4_quantize_mxfp4(ty, M, K, x.data_ptr(), ldx, rows, cols, _stream(stream)), "fp4_quantize_mxfp4")
+    _native.quantize(M, K, x, q, s, qt, st, stream)
 
 
 def fp4_dequant_mxfp4(M, K, q, s, out, stream=None):
     """The values of an MXFP4 operand into out [M, K] (float32 or bfloat16; rows may be strided)."""
-    ty = _dense_type(out, "out", {torch.float32: 1, torch.bfloat16: 2})
-    ldo = _rows_of(out, M, K, "out")
-    dev = _device(q, s, out)
-    a = _mx_struct(q, s, M, K, "operand")
-    with torch.cuda.device(dev):
-        _check(lib().fp4_dequant_mxfp4(ty, M, K, a, out.data_ptr(), ldo, _stream(stream)), "fp4_dequant_mxfp4")
+    _native.dequant(M, K, q, s, out, stream)
 
 
-@functools.lru_cache(maxsize=4096)
-def _mx_workspace_bytes(name: str, M: int, N: int, K: int, device: int) -> int:
-    with torch.cuda.device(device):
+def _mx_workspace_bytes(name, M, N, K, device) -> int:
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
         n = int(getattr(lib(), name)(M, N, K))
     _check(n if n < 0 else 0, name)
     return n
@@ -482,66 +428,23 @@ def _mx_workspace_bytes(name: str, M: int, N: int, K: int, device: int) -> int:
 
 def w4a4_matmul_workspace_bytes(M, N, K, device=None) -> int:
     """Workspace bytes w4a4_matmul can use for this shape on `device` (default: the current one)."""
-    return _mx_workspace_bytes("w4a4_matmul_workspace_bytes", M, N, K, _device_index(device))
+    return _mx_workspace_bytes("w4a4_matmul_workspace_bytes", M, N, K, device)
 
 
 def w4a4_linear_workspace_bytes(M, N, K, device=None) -> int:
     """Workspace bytes of w4a4_linear for this shape on `device` (default: the current one)."""
-    return _mx_workspace_bytes("w4a4_linear_workspace_bytes", M, N, K, _device_index(device))
-
-
-def _device_index(device) -> int:
-    if device is None:
-        return torch.cuda.current_device()
-    d = torch.device(device)
-    return d.index if d.index is not None else torch.cuda.current_device()
-
-
-def _mx_workspace(name, M, N, K, dev, stream, st, workspace):
-    """(pointer, bytes, tensor) of the given workspace or of one allocated here as the library asks."""
-    if workspace is None:
-        nbytes = _mx_workspace_bytes(name, M, N, K, dev.index) if M > 0 else 0
-        if nbytes == 0:
-            return None, 0, None
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        if stream is not None:
-            # the kernels run on `stream`, not necessarily the one the allocator recorded
-            ext = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(st)
-            workspace.record_stream(ext)
-    elif workspace.device != dev:
-        raise ValueError("the workspace must live on the tensors' GPU")
-    return _ptr(workspace), _nbytes(workspace), workspace
+    return _mx_workspace_bytes("w4a4_linear_workspace_bytes", M, N, K, device)
 
 
 def w4a4_matmul(M, N, K, aq, a_s, bq, bs, y, stream=None, workspace=None):
-    """y [M, N] (float32, bfloat16 or float16; rows may be strided) = A B^T of two MXFP4 operands of depth K."""
-    ty = _dense_type(y, "y")
-    ldy = _rows_of(y, M, N, "y")
-    dev = _device(aq, a_s, bq, bs, y)
-    a, b = _mx_struct(aq, a_s, M, K, "A"), _mx_struct(bq, bs, N, K, "B")
-    with torch.cuda.device(dev):
-        st = _stream(stream)
-        ws, nbytes, keep = _mx_workspace("w4a4_matmul_workspace_bytes", M, N, K, dev, stream, st, workspace)
-        _check(lib().w4a4_matmul(ty, M, N, K, a, b, y.data_ptr(), ldy, ws, nbytes, st), "w4a4_matmul")
+    """y [M, N] (float32, bfloat16 or float16; rows may be strided) = A B^T of two MXFP4 operands of depth K.
+    `workspace`: a uint8 CUDA tensor, by default one of the size the library asks for, allocated here."""
+    _native.matmul(M, N, K, aq, a_s, bq, bs, y, stream, workspace)
 
 
 def w4a4_linear(M, N, K, x, bq, bs, y, stream=None, workspace=None):
     """y [M, N] = Q(x) B^T: dense x [M, K] quantised along its rows, times an MXFP4 operand of depth K."""
-    tx, ty = _dense_type(x, "x"), _dense_type(y, "y")
-    ldx, ldy = _rows_of(x, M, K, "x"), _rows_of(y, M, N, "y")
-    dev = _device(x, bq, bs, y)
-    b = _mx_struct(bq, bs, N, K, "B")
-    with torch.cuda.device(dev):
-        st = _stream(stream)
-        ws, nbytes, keep = _mx_workspace("w4a4_linear_workspace_bytes", M, N, K, dev, stream, st, workspace)
-        _check(lib().w4a4_linear(tx, ty, M, N, K, x.data_ptr(), ldx, b, y.data_ptr(), ldy, ws, nbytes, st), "w4a4_linear")
-
-
-def _as_rows(x: torch.Tensor) -> torch.Tensor:
-    """x [..., K] as a matrix whose rows are contiguous (a copy only where the strides ask for one)."""
-    x = x.reshape(-1, x.shape[-1]) if x.dim() != 2 else x
-    ok = (x.shape[1] <= 1 or x.stride(1) == 1) and (x.shape[0] <= 1 or x.stride(0) >= x.shape[1])
-    return x if ok else x.contiguous()
+    _native.linear(M, N, K, x, bq, bs, y, stream, workspace)
 
 
 @dataclass
@@ -556,7 +459,7 @@ class MXTensor:
     def empty(rows: int, K: int, device="cuda") -> "MXTensor":
         if rows < 0 or K < 1:
             raise ValueError(f"an MXFP4 operand needs rows >= 0 and K >= 1, not {rows} and {K}")
-        nb = _blocks(K)
+        nb = (K + 31) // 32
         scales = torch.empty(rows, (nb + 3) // 4 * 4, dtype=torch.uint8, device=device)
         return MXTensor(torch.empty(rows, 16 * nb, dtype=torch.uint8, device=device), scales[:, :nb], rows, K)
 
@@ -564,133 +467,58 @@ class MXTensor:
     def from_canonical(codes: torch.Tensor, scales: torch.Tensor, K: int | None = None) -> "MXTensor":
         """Codes [rows, K / 2] and E8M0 scales [rows, K / 32] as checkpoints hold them. The tensors are used as they are
         where their rows are aligned (codes to 16 bytes, scales to 4), and copied otherwise."""
-        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
-            raise TypeError("codes and scales must be uint8")
-        if codes.dim() != 2 or scales.dim() != 2 or codes.shape[0] != scales.shape[0]:
-            raise ValueError("codes and scales must be matrices with the same number of rows")
-        K = codes.shape[1] * 2 if K is None else K
-        rows, nb = codes.shape[0], _blocks(K)
-        if K < 1 or codes.shape[1] != 16 * nb or scales.shape[1] != nb:
-            raise ValueError(f"K = {K} needs {16 * nb} bytes of codes and {nb} scales a row, "
-                             f"not {codes.shape[1]} and {scales.shape[1]}")
-        _device(codes, scales)
-        t = MXTensor.empty(rows, K, device=codes.device)
-        if codes.stride(1) == 1 and (rows <= 1 or (codes.stride(0) % 16 == 0 and codes.stride(0) >= 16 * nb)) \
-                and codes.data_ptr() % 16 == 0:
-            t.codes = codes
-        else:
-            t.codes.copy_(codes)
-        end = scales.storage_offset() + (rows - 1) * scales.stride(0) + (nb + 3) // 4 * 4
-        if (nb <= 1 or scales.stride(1) == 1) and (rows <= 1 or (scales.stride(0) % 4 == 0 and scales.stride(0) >= nb)) \
-                and scales.data_ptr() % 4 == 0 and end <= scales.untyped_storage().nbytes():
-            t.scales = scales
-        else:
-            t.scales.copy_(scales)
-        return t
+        return MXTensor(*_native.from_canonical(codes, scales, K))
 
     @staticmethod
     def quantize(x: torch.Tensor, stream=None) -> "MXTensor":
         """x [..., K] along its last axis."""
-        x = _as_rows(x)
-        t = MXTensor.empty(x.shape[0], x.shape[1], device=x.device)
-        fp4_quantize_mxfp4(x.shape[0], x.shape[1], x, t.codes, t.scales, stream=stream)
-        return t
+        rows, k, q, s, _, _ = _native.quantize_new(x, True, False, stream)
+        return MXTensor(q, s, rows, k)
 
     @staticmethod
     def quantize_t(x: torch.Tensor, stream=None) -> "MXTensor":
         """x [..., K], seen as a matrix, along its columns: the operand of K rows that stands for its transpose."""
-        x = _as_rows(x)
-        t = MXTensor.empty(x.shape[1], x.shape[0], device=x.device)
-        fp4_quantize_mxfp4(x.shape[0], x.shape[1], x, None, None, t.codes, t.scales, stream=stream)
-        return t
+        rows, k, _, _, q, s = _native.quantize_new(x, False, True, stream)
+        return MXTensor(q, s, k, rows)
 
     @staticmethod
     def quantize_both(x: torch.Tensor, stream=None) -> tuple["MXTensor", "MXTensor"]:
         """(quantize(x), quantize_t(x)) from one reading of x."""
-        x = _as_rows(x)
-        r = MXTensor.empty(x.shape[0], x.shape[1], device=x.device)
-        c = MXTensor.empty(x.shape[1], x.shape[0], device=x.device)
-        fp4_quantize_mxfp4(x.shape[0], x.shape[1], x, r.codes, r.scales, c.codes, c.scales, stream=stream)
-        return r, c
+        rows, k, q, s, qt, st = _native.quantize_new(x, True, True, stream)
+        return MXTensor(q, s, rows, k), MXTensor(qt, st, k, rows)
 
     def dequant(self, dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
         out = torch.empty(self.rows, self.K, dtype=dtype, device=self.codes.device)
-        fp4_dequant_mxfp4(self.rows, self.K, self.codes, self.scales, out, stream)
+        _native.dequant(self.rows, self.K, self.codes, self.scales, out, stream)
         return out
 
     def matmul(self, x, out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
                stream=None, workspace: torch.Tensor | None = None) -> torch.Tensor:
         """x self^T [M, rows], self the weights: x an MXTensor of the same K, or dense [M, K], quantised on the way."""
-        if isinstance(x, MXTensor):
-            if x.K != self.K:
-                raise ValueError(f"depths differ: {x.K} and {self.K}")
-            m = x.rows
+        packed = isinstance(x, MXTensor)
+        if packed:
+            m, k = x.rows, x.K
         else:
-            if x.dim() != 2 or x.shape[1] != self.K:
+            if x.dim() != 2:
                 raise ValueError("x must be [M, K] with the weights' K")
-            m = x.shape[0]
+            m, k = x.shape
+        if k != self.K:
+            raise ValueError(f"depths differ: {k} and {self.K}")
         if out is None:
             out = torch.empty(m, self.rows, dtype=out_dtype, device=self.codes.device)
-        if isinstance(x, MXTensor):
-            w4a4_matmul(m, self.rows, self.K, x.codes, x.scales, self.codes, self.scales, out, stream, workspace)
+        if packed:
+            _native.matmul(m, self.rows, k, x.codes, x.scales, self.codes, self.scales, out, stream, workspace)
         else:
-            w4a4_linear(m, self.rows, self.K, _as_rows(x), self.codes, self.scales, out, stream, workspace)
+            if x.stride(1) != 1 and k > 1 or m > 1 and x.stride(0) < k:
+                x = x.contiguous()
+            _native.linear(m, self.rows, k, x, self.codes, self.scales, out, stream, workspace)
         return out
 
 
-class _MxLinear(torch.autograd.Function):
-    """y = Q(x) Q(w)^T. Rounding to MXFP4 counts as the identity in the backward pass, whose products are MXFP4 too:
-    dx = Q(g) Q(w^T)^T contracts N, dw = Q(g^T) Q(x^T)^T contracts the rows of x, each operand quantised along the axis
-    contracted. The transposed operands are made with the forward ones, from one reading of x and of w."""
-
-    @staticmethod
-    def forward(ctx, x, w):
-        rows = _as_rows(x)
-        need_dx, need_dw = ctx.needs_input_grad
-        ctx.shape, ctx.w_dtype, ctx.x_dtype = x.shape, w.dtype, x.dtype
-        xq, xt = MXTensor.quantize_both(rows) if need_dw and rows.shape[0] else (MXTensor.quantize(rows), None)
-        wm = _as_rows(w)
-        wq, wt = MXTensor.quantize_both(wm) if need_dx else (MXTensor.quantize(wm), None)
-        empty = torch.empty(0, dtype=torch.uint8, device=x.device)
-        ctx.save_for_backward(xt.codes if xt else empty, xt.scales if xt else empty, wt.codes if wt else empty,
-                              wt.scales if wt else empty)
-        return wq.matmul(xq, out_dtype=x.dtype).reshape(*x.shape[:-1], w.shape[0])
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, g):
-        xc, xs, wc, ws = ctx.saved_tensors
-        g = _as_rows(g)
-        m, n = g.shape
-        k = ctx.shape[-1]
-        need_dx, need_dw = ctx.needs_input_grad
-        dx = dw = None
-        if m == 0:
-            dx = torch.empty(ctx.shape, dtype=ctx.x_dtype, device=g.device) if need_dx else None
-            dw = torch.zeros(n, k, dtype=ctx.w_dtype, device=g.device) if need_dw else None
-            return dx, dw
-        gq = gt = None
-        if need_dx and need_dw:
-            gq, gt = MXTensor.quantize_both(g)
-        elif need_dx:
-            gq = MXTensor.quantize(g)
-        elif need_dw:
-            gt = MXTensor.quantize_t(g)
-        if need_dx:
-            dx = MXTensor(wc, ws, k, n).matmul(gq, out_dtype=ctx.x_dtype).reshape(ctx.shape)
-        if need_dw:
-            dw = MXTensor(xc, xs, k, m).matmul(gt, out_dtype=ctx.w_dtype)
-        return dx, dw
-
-
 def mx_linear(x: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
-    """x [..., K] times w [N, K] transposed, both quantised to MXFP4 in the call, in x's type; differentiable in both.
-    x and w are float32, bfloat16 or float16 on one GPU; dx has x's type and dw has w's."""
-    _dense_type(x, "x")
-    _dense_type(w, "w")
-    _device(x, w)
-    if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1]:
-        raise ValueError(f"x [..., K] and w [N, K] expected, not {list(x.shape)} and {list(w.shape)}")
-    if w.shape[0] < 1 or w.shape[1] < 1:
-        raise ValueError("w has no rows or no columns")
-    return _MxLinear.apply(x, w)
+    """x [..., K] times w [N, K] transposed, both quantised to MXFP4 in the call, in x's type; differentiable once in both.
+
+    Rounding to MXFP4 counts as the identity in the backward pass, whose products are MXFP4 too: with g the gradient of
+    the result, dx = Q(g) Q(w^T)^T in x's type and dw = Q(g^T) Q(x^T)^T in w's, every operand quantised along the axis that
+    its product contracts. x and w are float32, bfloat16 or float16 on one GPU."""
+    return _native.mx_linear(x, w)

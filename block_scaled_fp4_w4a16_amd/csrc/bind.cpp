@@ -1,0 +1,326 @@
+// Native half of the Python binding of the MXFP4 operators: argument checks, allocation through torch and the calls of
+// the C entry points, and the trainable layer's autograd node. A decode-sized product runs for a few microseconds;
+// the same checks written in Python took 23 to 30 microseconds a call.
+#include <ATen/ATen.h>
+#include <c10/core/DeviceGuard.h>
+#include <c10/hip/HIPStream.h>
+#include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/utils/pybind.h>
+
+#include "fp4w4a16.h"
+
+namespace py = pybind11;
+using at::Tensor;
+using OptTensor = std::optional<Tensor>;
+
+namespace {
+
+template <typename... A>
+[[noreturn]] void type_error(const A&... a) {
+  throw py::type_error(c10::str(a...));
+}
+template <typename... A>
+[[noreturn]] void value_error(const A&... a) {
+  throw py::value_error(c10::str(a...));
+}
+
+int64_t blocks_of(int64_t k) { return (k + 31) / 32; }
+
+int dense_type(const Tensor& t, const char* what, bool half = true) {
+  switch (t.scalar_type()) {
+    case at::kFloat: return FP4_TYPE_F32;
+    case at::kBFloat16: return FP4_TYPE_BF16;
+    case at::kHalf:
+      if (half) return FP4_TYPE_F16;
+      [[fallthrough]];
+    default: type_error(what, " must be float32", half ? ", bfloat16 or float16" : " or bfloat16", ", not ", t.scalar_type());
+  }
+}
+
+// Row stride (in elements) of a rows x cols matrix whose rows are contiguous and do not overlap.
+int64_t rows_of(const Tensor& t, int64_t rows, int64_t cols, const char* what) {
+  if (t.dim() != 2 || t.size(0) != rows || t.size(1) != cols)
+    value_error(what, " must have shape [", rows, ", ", cols, "], not ", t.sizes());
+  if (cols > 1 && t.stride(1) != 1) value_error(what, ": the elements of a row must be contiguous");
+  if (rows > 1 && t.stride(0) < cols) value_error(what, ": rows overlap");
+  return rows > 1 ? t.stride(0) : std::max<int64_t>(cols, 1);
+}
+
+fp4_mx operand(const Tensor& q, const Tensor& s, int64_t rows, int64_t k, const char* what) {
+  if (q.scalar_type() != at::kByte || s.scalar_type() != at::kByte) type_error(what, ": codes and scales must be uint8");
+  const int64_t nb = blocks_of(k), padded = (nb + 3) / 4 * 4;
+  const int64_t ldq = rows_of(q, rows, 16 * nb, what);
+  int64_t lds = rows_of(s, rows, nb, what);
+  if (rows == 1) lds = padded;
+  // rows of scales are read in whole dwords
+  if (rows > 0 && s.storage_offset() + (rows - 1) * lds + padded > (int64_t)s.storage().nbytes())
+    value_error(what, ": the last row of scales must be readable up to a multiple of 4 bytes");
+  return {q.data_ptr(), s.data_ptr(), ldq, lds};
+}
+
+c10::Device one_device(std::initializer_list<const Tensor*> ts) {
+  const c10::Device d = (*ts.begin())->device();
+  for (const Tensor* t : ts)
+    if (t->device() != d) value_error("tensors must all live on one GPU (got ", d, " and ", t->device(), ")");
+  if (!d.is_cuda()) value_error("tensors must live on the GPU");
+  return d;
+}
+
+void check(int64_t rc, const char* what) {
+  if (rc < 0) throw std::runtime_error(c10::str(what, ": ", fp4_status_string((int)rc), " (status ", rc, ")"));
+}
+
+// The caller's stream: None (the device's current one), a torch stream or a raw handle.
+struct Stream {
+  void* raw;
+  bool given;
+};
+Stream stream_of(const py::handle& stream, c10::Device d) {
+  if (stream.is_none()) return {c10::hip::getCurrentHIPStream(d.index()).stream(), false};
+  const py::object h = py::hasattr(stream, "cuda_stream") ? py::object(stream.attr("cuda_stream")) : py::reinterpret_borrow<py::object>(stream);
+  return {reinterpret_cast<void*>(h.cast<uintptr_t>()), true};
+}
+Stream current(c10::Device d) { return {c10::hip::getCurrentHIPStream(d.index()).stream(), false}; }
+
+struct Workspace {
+  Tensor hold;
+  void* p = nullptr;
+  size_t bytes = 0;
+};
+// The given workspace, or one of `need` bytes from torch's allocator, kept from reuse until `st` is done with it.
+Workspace workspace_of(const OptTensor& given, int64_t need, c10::Device d, const Stream& st) {
+  Workspace w;
+  if (given) {
+    if (given->device() != d) value_error("the workspace must live on the tensors' GPU");
+    if (!given->is_contiguous()) value_error("tensors must be contiguous");
+    w.hold = *given;
+  } else if (need > 0) {
+    w.hold = at::empty({need}, at::TensorOptions().dtype(at::kByte).device(d));
+    if (st.given) {
+      const c10::StreamId id = c10::hip::getStreamFromExternal((hipStream_t)st.raw, d.index()).id();
+      w.hold.record_stream(c10::Stream(c10::Stream::UNSAFE, d, id));
+    }
+  } else {
+    return w;
+  }
+  w.p = w.hold.data_ptr();
+  w.bytes = w.hold.nbytes();
+  return w;
+}
+
+// ------------------------------------------------------------------------------------------------ operators
+
+void quantize_into(int64_t M, int64_t K, const Tensor& x, const Tensor* q, const Tensor* s, const Tensor* qt, const Tensor* st_,
+                   const Stream& st, c10::Device d) {
+  const int type = dense_type(x, "x");
+  const int64_t ldx = rows_of(x, M, K, "x");
+  fp4_mx rows{}, cols{};
+  if (q) rows = operand(*q, *s, M, K, "rows");
+  if (qt) cols = operand(*qt, *st_, K, M, "columns");
+  c10::DeviceGuard guard(d);
+  check(fp4_quantize_mxfp4(type, M, K, x.data_ptr(), ldx, q ? &rows : nullptr, qt ? &cols : nullptr, st.raw),
+        "fp4_quantize_mxfp4");
+}
+
+void quantize(int64_t M, int64_t K, const Tensor& x, const OptTensor& q, const OptTensor& s, const OptTensor& qt,
+              const OptTensor& st_, const py::object& stream) {
+  dense_type(x, "x");
+  if (q.has_value() != s.has_value() || qt.has_value() != st_.has_value()) value_error("codes and scales come in pairs");
+  rows_of(x, M, K, "x");
+  const c10::Device d = one_device({&x, q ? &*q : &x, s ? &*s : &x, qt ? &*qt : &x, st_ ? &*st_ : &x});
+  quantize_into(M, K, x, q ? &*q : nullptr, s ? &*s : nullptr, qt ? &*qt : nullptr, st_ ? &*st_ : nullptr,
+                stream_of(stream, d), d);
+}
+
+struct Operand {
+  Tensor codes, scales;
+};
+
+Operand new_operand(int64_t rows, int64_t k, c10::Device d) {
+  if (rows < 0 || k < 1) value_error("an MXFP4 operand needs rows >= 0 and K >= 1, not ", rows, " and ", k);
+  const auto opt = at::TensorOptions().dtype(at::kByte).device(d);
+  const int64_t nb = blocks_of(k), padded = (nb + 3) / 4 * 4;
+  Operand o{at::empty({rows, 16 * nb}, opt), at::empty({rows, padded}, opt)};
+  if (padded != nb) o.scales = o.scales.narrow(1, 0, nb);
+  return o;
+}
+
+// x [..., K] as a matrix whose rows are contiguous (a copy only where the strides ask for one).
+Tensor as_rows(const Tensor& x) {
+  if (x.dim() < 1) value_error("a tensor with at least one axis expected");
+  Tensor m = x.dim() == 2 ? x : x.size(-1) > 0 ? x.reshape({x.numel() / x.size(-1), x.size(-1)}) : x.reshape({-1, 0});
+  const bool ok = (m.size(1) <= 1 || m.stride(1) == 1) && (m.size(0) <= 1 || m.stride(0) >= m.size(1));
+  return ok ? m : m.contiguous();
+}
+
+using Quantized = std::pair<Operand, Operand>;
+
+Quantized quantize_new(const Tensor& m, bool rows, bool cols, const Stream& st, c10::Device d) {
+  Quantized r;
+  if (rows) r.first = new_operand(m.size(0), m.size(1), d);
+  if (cols) r.second = new_operand(m.size(1), m.size(0), d);
+  quantize_into(m.size(0), m.size(1), m, rows ? &r.first.codes : nullptr, rows ? &r.first.scales : nullptr,
+                cols ? &r.second.codes : nullptr, cols ? &r.second.scales : nullptr, st, d);
+  return r;
+}
+
+// (rows, K, codes, scales, codes along the columns, their scales)
+py::tuple quantize_py(const Tensor& x, bool rows, bool cols, const py::object& stream) {
+  dense_type(x, "x");
+  const c10::Device d = one_device({&x});
+  const Tensor m = as_rows(x);
+  const Quantized r = quantize_new(m, rows, cols, stream_of(stream, d), d);
+  return py::make_tuple(m.size(0), m.size(1), r.first.codes, r.first.scales, r.second.codes, r.second.scales);
+}
+
+void dequant(int64_t M, int64_t K, const Tensor& q, const Tensor& s, const Tensor& out, const py::object& stream) {
+  const int type = dense_type(out, "out", false);
+  const int64_t ldo = rows_of(out, M, K, "out");
+  const c10::Device d = one_device({&q, &s, &out});
+  const fp4_mx a = operand(q, s, M, K, "operand");
+  c10::DeviceGuard guard(d);
+  check(fp4_dequant_mxfp4(type, M, K, &a, out.data_ptr(), ldo, stream_of(stream, d).raw), "fp4_dequant_mxfp4");
+}
+
+void matmul_into(int64_t M, int64_t N, int64_t K, const Operand& A, const Operand& B, const Tensor& y, const Stream& st,
+                 const OptTensor& ws, c10::Device d) {
+  const int type = dense_type(y, "y");
+  const int64_t ldy = rows_of(y, M, N, "y");
+  const fp4_mx a = operand(A.codes, A.scales, M, K, "A"), b = operand(B.codes, B.scales, N, K, "B");
+  c10::DeviceGuard guard(d);
+  const int64_t need = ws ? 0 : w4a4_matmul_workspace_bytes(M, N, K);
+  check(need, "w4a4_matmul");
+  const Workspace w = workspace_of(ws, need, d, st);
+  check(w4a4_matmul(type, M, N, K, &a, &b, y.data_ptr(), ldy, w.p, w.bytes, st.raw), "w4a4_matmul");
+}
+
+void matmul(int64_t M, int64_t N, int64_t K, const Tensor& aq, const Tensor& as, const Tensor& bq, const Tensor& bs,
+            const Tensor& y, const py::object& stream, const OptTensor& ws) {
+  const c10::Device d = one_device({&aq, &as, &bq, &bs, &y});
+  matmul_into(M, N, K, {aq, as}, {bq, bs}, y, stream_of(stream, d), ws, d);
+}
+
+void linear_into(int64_t M, int64_t N, int64_t K, const Tensor& x, const Operand& B, const Tensor& y, const Stream& st,
+                 const OptTensor& ws, c10::Device d) {
+  const int tx = dense_type(x, "x"), ty = dense_type(y, "y");
+  const int64_t ldx = rows_of(x, M, K, "x"), ldy = rows_of(y, M, N, "y");
+  const fp4_mx b = operand(B.codes, B.scales, N, K, "B");
+  c10::DeviceGuard guard(d);
+  const int64_t need = ws ? 0 : w4a4_linear_workspace_bytes(M, N, K);
+  check(need, "w4a4_linear");
+  const Workspace w = workspace_of(ws, need, d, st);
+  check(w4a4_linear(tx, ty, M, N, K, x.data_ptr(), ldx, &b, y.data_ptr(), ldy, w.p, w.bytes, st.raw), "w4a4_linear");
+}
+
+void linear(int64_t M, int64_t N, int64_t K, const Tensor& x, const Tensor& bq, const Tensor& bs, const Tensor& y,
+            const py::object& stream, const OptTensor& ws) {
+  const c10::Device d = one_device({&x, &bq, &bs, &y});
+  linear_into(M, N, K, x, {bq, bs}, y, stream_of(stream, d), ws, d);
+}
+
+// Codes and scales used as they are where their rows are aligned (16 and 4 bytes), else copied.
+py::tuple from_canonical(const Tensor& codes, const Tensor& scales, std::optional<int64_t> K) {
+  if (codes.scalar_type() != at::kByte || scales.scalar_type() != at::kByte) type_error("codes and scales must be uint8");
+  if (codes.dim() != 2 || scales.dim() != 2 || codes.size(0) != scales.size(0))
+    value_error("codes and scales must be matrices with the same number of rows");
+  const int64_t k = K ? *K : 2 * codes.size(1), rows = codes.size(0), nb = blocks_of(k), padded = (nb + 3) / 4 * 4;
+  if (k < 1 || codes.size(1) != 16 * nb || scales.size(1) != nb)
+    value_error("K = ", k, " needs ", 16 * nb, " bytes of codes and ", nb, " scales a row, not ", codes.size(1), " and ",
+                scales.size(1));
+  const c10::Device d = one_device({&codes, &scales});
+  const auto aligned = [&](const Tensor& t, int64_t cols, uintptr_t a) {
+    return (cols <= 1 || t.stride(1) == 1) && (rows <= 1 || (t.stride(0) % (int64_t)a == 0 && t.stride(0) >= cols)) &&
+           (uintptr_t)t.data_ptr() % a == 0;
+  };
+  const auto opt = at::TensorOptions().dtype(at::kByte).device(d);
+  Tensor q = codes, s = scales;
+  if (!aligned(q, 16 * nb, 16)) q = at::empty({rows, 16 * nb}, opt).copy_(codes);
+  const int64_t end = s.storage_offset() + std::max<int64_t>(rows - 1, 0) * s.stride(0) + padded;
+  if (!aligned(s, nb, 4) || end > (int64_t)s.storage().nbytes())
+    s = at::empty({rows, padded}, opt).narrow(1, 0, nb).copy_(scales);
+  return py::make_tuple(q, s, rows, k);
+}
+
+// ------------------------------------------------------------------------------------------- trainable layer
+
+// y = Q(x) Q(w)^T. Rounding to MXFP4 counts as the identity in the backward pass, whose products are MXFP4 too:
+// dx = Q(g) Q(w^T)^T contracts N, dw = Q(g^T) Q(x^T)^T contracts the rows of x, each operand quantised along the axis
+// contracted. The transposed operands are made with the forward ones, from one reading of x and of w.
+struct MxLinear : torch::autograd::Function<MxLinear> {
+  static Tensor forward(torch::autograd::AutogradContext* ctx, const Tensor& x, const Tensor& w, bool need_dx, bool need_dw) {
+    const c10::Device d = x.device();
+    const Stream st = current(d);
+    const Tensor xm = as_rows(x), wm = as_rows(w);
+    const int64_t m = xm.size(0), k = xm.size(1), n = wm.size(0);
+    std::vector<int64_t> shape = x.sizes().vec();
+    shape.back() = n;
+    Tensor y = at::empty(shape, x.options().requires_grad(false).memory_format(at::MemoryFormat::Contiguous));
+    Operand xt, wt;
+    if (m > 0) {
+      Quantized wq = quantize_new(wm, true, need_dx, st, d), xq = quantize_new(xm, true, need_dw, st, d);
+      matmul_into(m, n, k, xq.first, wq.first, y.view({m, n}), st, {}, d);
+      wt = std::move(wq.second), xt = std::move(xq.second);
+    }
+    ctx->save_for_backward({xt.codes, xt.scales, wt.codes, wt.scales});
+    ctx->saved_data["shape"] = x.sizes().vec();
+    ctx->saved_data["types"] = std::vector<int64_t>{(int64_t)x.scalar_type(), (int64_t)w.scalar_type()};
+    return y;
+  }
+
+  static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx, torch::autograd::variable_list grads) {
+    const bool need_dx = ctx->needs_input_grad(0), need_dw = ctx->needs_input_grad(1);
+    const auto shape = ctx->saved_data["shape"].toIntVector();
+    const auto types = ctx->saved_data["types"].toIntVector();
+    const Tensor g = as_rows(grads[0]);
+    const int64_t m = g.size(0), n = g.size(1), k = shape.back();
+    const c10::Device d = g.device();
+    const auto opt = at::TensorOptions().device(d);
+    Tensor dx, dw;
+    if (need_dx) dx = at::empty(shape, opt.dtype((at::ScalarType)types[0]));
+    if (need_dw) dw = at::empty({n, k}, opt.dtype((at::ScalarType)types[1]));
+    if (m == 0) {
+      if (need_dw) dw.zero_();
+    } else if (need_dx || need_dw) {
+      const Stream st = current(d);
+      const Quantized q = quantize_new(g, need_dx, need_dw, st, d);
+      const auto saved = ctx->get_saved_variables();
+      if (need_dx) matmul_into(m, k, n, q.first, {saved[2], saved[3]}, dx.view({m, k}), st, {}, d);
+      if (need_dw) matmul_into(n, k, m, q.second, {saved[0], saved[1]}, dw, st, {}, d);
+    }
+    torch::autograd::variable_list out{dx, dw, Tensor(), Tensor()};
+    if (at::GradMode::is_enabled()) {  // create_graph: the gradients have no derivative, and asking for one is an error
+      for (Tensor* t : {&dx, &dw})
+        if (t->defined()) *t = t->detach().requires_grad_();
+      const auto error = std::make_shared<torch::autograd::DelayedError>("mx_linear is differentiable once", 2);
+      torch::autograd::variable_list both = error->apply({dx, dw});
+      out[0] = both[0], out[1] = both[1];
+    }
+    return out;
+  }
+};
+
+Tensor mx_linear(const Tensor& x, const Tensor& w) {
+  dense_type(x, "x");
+  dense_type(w, "w");
+  if (x.dim() < 1 || w.dim() != 2 || x.size(-1) != w.size(1))
+    value_error("x [..., K] and w [N, K] expected, not ", x.sizes(), " and ", w.sizes());
+  if (w.size(0) < 1 || w.size(1) < 1) value_error("w has no rows or no columns");
+  one_device({&x, &w});
+  const bool grad = at::GradMode::is_enabled();
+  const bool need_dx = grad && x.requires_grad(), need_dw = grad && w.requires_grad();
+  py::gil_scoped_release release;
+  return MxLinear::apply(x, w, need_dx, need_dw);
+}
+
+}  // namespace
+
+PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
+  m.def("quantize", &quantize);
+  m.def("quantize_new", &quantize_py);
+  m.def("dequant", &dequant);
+  m.def("matmul", &matmul);
+  m.def("linear", &linear);
+  m.def("from_canonical", &from_canonical);
+  m.def("mx_linear", &mx_linear);
+}

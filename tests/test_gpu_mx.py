@@ -460,6 +460,34 @@ def test_layer_partial_gradients_shapes_and_no_rows():
     assert y.shape == (0, 40) and dx.shape == (0, 64) and not dw.any()
 
 
+def test_layer_twice_and_in_place():
+    x = dense(24, 64, torch.bfloat16, 63).cuda().requires_grad_()
+    w = dense(40, 64, torch.float32, 64).cuda().requires_grad_()
+    g = dense(24, 40, torch.bfloat16, 65).cuda()
+    want = torch.autograd.grad(fp4.mx_linear(x, w), (x, w), g)
+    y = fp4.mx_linear(x, w)
+    for a, b in zip(torch.autograd.grad(y, (x, w), g, retain_graph=True), want):
+        assert torch.equal(a, b)
+    for a, b in zip(torch.autograd.grad(y, (x, w), g), want):
+        assert torch.equal(a, b)
+    with pytest.raises(RuntimeError):                          # freed
+        torch.autograd.grad(y, (x, w), g)
+    y = fp4.mx_linear(x, w).mul_(2.0)
+    for a, b in zip(torch.autograd.grad(y, (x, w), g / 2), want):
+        assert torch.equal(a, b)
+    # differentiable once: a second derivative is an error, not a zero
+    dx, dw = torch.autograd.grad(fp4.mx_linear(x, w), (x, w), g, create_graph=True)
+    assert torch.equal(dx, want[0])
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(dx.float().sum() + dw.sum(), x)
+    with pytest.raises(RuntimeError, match="once"):
+        (dx.float().sum() + dw.sum()).backward()
+    (dw,) = torch.autograd.grad(fp4.mx_linear(x.detach(), w), w, g, create_graph=True)
+    assert torch.equal(dw, want[1])
+    with torch.no_grad():
+        assert not fp4.mx_linear(x, w).requires_grad
+
+
 def test_a_few_layers_together():
     # prefill through a gated pair of projections in both forms: quantised once for two products, or dense
     m, k, f = 70, 256, 300
