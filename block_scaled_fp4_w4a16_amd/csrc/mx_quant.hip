@@ -117,151 +117,209 @@ int launch_quantize_rows(int type, int64_t M, int64_t K, const void* x, int64_t 
 }
 
 // ---------------------------------------------------------------------- along the columns, or along both axes
-// A lane holds a patch of 32 rows x C columns in registers (C = 16 bytes of a row: 8 or 4 values). Down its columns
-// every block is the lane's own: no exchange. Along its rows a block is 4 (16-bit types) or 8 (FP32) neighbouring
-// lanes. A wave covers 4 patches down and 16 across: 128 rows x 128 (64) columns. Both results come from the one
-// reading of x.
-template <int T, bool ROWS>
-__global__ void __launch_bounds__(256) quantize_cols_kernel(const void* __restrict__ x, int64_t ldx, fp4_mx rows, fp4_mx cols,
-                                                            int M, int K, int tiles_k, int64_t tiles) {
-  constexpr int EB = elem_bytes(T), C = 16 / EB, WC = 16 * C;
-  const int lane = threadIdx.x & 63;
-  const int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (tile >= tiles) return;
-  const int tm = (int)(tile / tiles_k), tk = (int)(tile % tiles_k);
-  const int cg = lane & 15, mb = lane >> 4;
-  const int col0 = tk * WC, col = col0 + cg * C;
-  const int row0 = tm * 128 + mb * 32;
-  const uint8_t* p = static_cast<const uint8_t*>(x) + ((int64_t)row0 * ldx + col) * EB;
-  u32x4 v[32];
-  if (tm * 128 + 128 <= M && col0 + WC <= K) {
+// A lane holds a patch of 32 rows x 4 columns in registers, a wave 32 rows x 256 columns, the W waves of a workgroup
+// 32 W rows. Down its columns every block is a lane's own, with no exchange; the results (16 bytes per column and wave)
+// meet in LDS, so that a column's 16 W bytes leave as whole lines. Along the rows a block is 8 neighbouring lanes; a
+// 4 x 4 exchange within each quad of lanes turns four rows' 2 bytes per lane into 8 bytes of one row, so that a store
+// writes 128 bytes of each of four rows. Both results come from the one reading of x.
+template <int T>
+struct Patch {
+  static constexpr int R = T == FP4_TYPE_F32 ? 4 : 2;  // registers per row
+  uint32_t v[32][R];
+  // the largest magnitude of column c (a 16-bit type: as amax_bits16 takes it)
+  __device__ __forceinline__ void column_max(uint32_t (&m)[4]) const {
+    if constexpr (T == FP4_TYPE_F32) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = load16(p + (int64_t)i * ldx * EB);
+      for (int c = 0; c < 4; ++c) {
+        m[c] = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) m[c] = max(m[c], v[i][c] & 0x7fffffffu);
+      }
+    } else {
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w = max_u16x2(w, v[i][p] & 0x7fff7fffu);
+        m[2 * p] = amax_bits16<T>(w & 0xffffu);
+        m[2 * p + 1] = amax_bits16<T>(w >> 16);
+      }
+    }
+  }
+  // codes of rows 2 i and 2 i + 1 of column C into byte B of `code`
+  template <int C, int B>
+  __device__ __forceinline__ uint32_t column_pair(uint32_t code, int i, float scale) const {
+    if constexpr (T == FP4_TYPE_F32) return cvt_pair32<B>(code, v[2 * i][C], v[2 * i + 1][C], scale);
+    else
+      return cvt_pair16<T, B>(code, __builtin_amdgcn_perm(v[2 * i + 1][C >> 1], v[2 * i][C >> 1], C & 1 ? 0x07060302u : 0x05040100u),
+                              scale);
+  }
+  template <int C>
+  __device__ __forceinline__ u32x4 column(float scale, uint32_t mask) const {
+    u32x4 out;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      uint32_t code = column_pair<C, 0>(0, 4 * d, scale);
+      code = column_pair<C, 1>(code, 4 * d + 1, scale);
+      code = column_pair<C, 2>(code, 4 * d + 2, scale);
+      code = column_pair<C, 3>(code, 4 * d + 3, scale);
+      out[d] = code & mask;
+    }
+    return out;
+  }
+  // row i: the scale byte of its block (8 lanes) and this lane's four codes
+  __device__ __forceinline__ void row(int i, uint32_t& sb, uint32_t& code) const {
+    uint32_t m;
+    if constexpr (T == FP4_TYPE_F32)
+      m = max(max(v[i][0] & 0x7fffffffu, v[i][1] & 0x7fffffffu), max(v[i][2] & 0x7fffffffu, v[i][3] & 0x7fffffffu));
+    else
+      m = max_u16x2(v[i][0] & 0x7fff7fffu, v[i][1] & 0x7fff7fffu), m = max(m & 0xffffu, m >> 16);
+    m = quad_max(m);
+    m = max(m, dpp<DPP_HALF_MIRROR>(m));
+    if constexpr (T != FP4_TYPE_F32) m = amax_bits16<T>(m);
+    sb = scale_byte(m);
+    const float sc = scale_value(sb);
+    if constexpr (T == FP4_TYPE_F32) code = cvt_pair32<1>(cvt_pair32<0>(0, v[i][0], v[i][1], sc), v[i][2], v[i][3], sc);
+    else code = cvt_pair16<T, 1>(cvt_pair16<T, 0>(0, v[i][0], sc), v[i][1], sc);
+    code &= code_mask(sb);
+  }
+};
+
+template <int T, int W, bool ROWS>
+__global__ void __launch_bounds__(64 * W) quantize_cols_kernel(const void* __restrict__ x, int64_t ldx, fp4_mx rows, fp4_mx cols,
+                                                               int M, int K, int tiles_k) {
+  constexpr int EB = elem_bytes(T), R = Patch<T>::R;
+  __shared__ u32x4 col_codes[256 * W];
+  __shared__ uint8_t col_scales[256 * W];
+  __shared__ uint8_t row_scales[ROWS ? W * 256 : 16];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tm = blockIdx.x / tiles_k, tk = blockIdx.x - tm * tiles_k;
+  const int col0 = 256 * tk, col = col0 + 4 * lane;
+  const int row0 = 32 * (W * tm + wave);
+
+  Patch<T> p;
+  const uint8_t* base = static_cast<const uint8_t*>(x) + (int64_t)col * EB;
+  if (col + 4 <= K) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      __builtin_memcpy(p.v[i], base + (int64_t)min(row0 + i, M - 1) * ldx * EB, 4 * EB);
   } else {
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      u32x4 w = {0, 0, 0, 0};
-      if (row0 + i < M) {
-        const uint8_t* r = p + (int64_t)i * ldx * EB;
+      const uint8_t* r = base + (int64_t)min(row0 + i, M - 1) * ldx * EB;
 #pragma unroll
-        for (int j = 0; j < C; ++j)
-          if (col + j < K) {
-            if constexpr (T == FP4_TYPE_F32) w[j] = reinterpret_cast<const uint32_t*>(r)[j];
-            else w[j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(r)[j] << (16 * (j & 1));
-          }
-      }
-      v[i] = w;
+      for (int j = 0; j < R; ++j) p.v[i][j] = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (col + j < K) {
+          if constexpr (T == FP4_TYPE_F32) p.v[i][j] = reinterpret_cast<const uint32_t*>(r)[j];
+          else p.v[i][j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(r)[j] << (16 * (j & 1));
+        }
     }
   }
+  if (row0 + 32 > M) {  // rows past the last one count as zeros
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+#pragma unroll
+      for (int j = 0; j < R; ++j) p.v[i][j] = row0 + i < M ? p.v[i][j] : 0u;
+  }
 
-  // down the columns
+  // down the columns: block `wave` of column c sits in slot wave ^ (c / 4 % W) of its 16 W bytes of LDS, so that
+  // neither the writes (one slot of columns 4 lane + j) nor the reads (all slots of a column) meet in a bank
   {
-    auto* q = static_cast<uint8_t*>(cols.q);
-    auto* s = static_cast<uint8_t*>(cols.s);
-    const int bm = tm * 4 + mb;
-    const bool live = row0 < M;
+    uint32_t m[4], sb[4];
+    p.column_max(m);
+    const int slot = 4 * W * lane + (wave ^ (lane & (W - 1)));
 #pragma unroll
-    for (int p4 = 0; p4 < 4; ++p4) {
-      uint32_t m = 0;
-      if constexpr (T == FP4_TYPE_F32) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) m = max(m, v[i][p4] & 0x7fffffffu);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) m = max_u16x2(m, v[i][p4] & 0x7fff7fffu);
-      }
-#pragma unroll
-      for (int h = 0; h < (T == FP4_TYPE_F32 ? 1 : 2); ++h) {
-        const int cc = T == FP4_TYPE_F32 ? p4 : 2 * p4 + h;
-        uint32_t bits;
-        if constexpr (T == FP4_TYPE_F32) bits = m;
-        else bits = amax_bits16<T>(h ? m >> 16 : m & 0xffffu);
-        const uint32_t sb = scale_byte(bits);
-        const float sc = scale_value(sb);
-        u32x4 out;
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          uint32_t code = 0;
-          if constexpr (T == FP4_TYPE_F32) {
-            code = cvt_pair32<0>(code, v[8 * d][p4], v[8 * d + 1][p4], sc);
-            code = cvt_pair32<1>(code, v[8 * d + 2][p4], v[8 * d + 3][p4], sc);
-            code = cvt_pair32<2>(code, v[8 * d + 4][p4], v[8 * d + 5][p4], sc);
-            code = cvt_pair32<3>(code, v[8 * d + 6][p4], v[8 * d + 7][p4], sc);
-          } else {
-            const uint32_t sel = h ? 0x07060302u : 0x05040100u;
-            code = cvt_pair16<T, 0>(code, __builtin_amdgcn_perm(v[8 * d + 1][p4], v[8 * d][p4], sel), sc);
-            code = cvt_pair16<T, 1>(code, __builtin_amdgcn_perm(v[8 * d + 3][p4], v[8 * d + 2][p4], sel), sc);
-            code = cvt_pair16<T, 2>(code, __builtin_amdgcn_perm(v[8 * d + 5][p4], v[8 * d + 4][p4], sel), sc);
-            code = cvt_pair16<T, 3>(code, __builtin_amdgcn_perm(v[8 * d + 7][p4], v[8 * d + 6][p4], sel), sc);
-          }
-          out[d] = code & code_mask(sb);
-        }
-        if (live && col + cc < K) {
-          *reinterpret_cast<u32x4*>(q + (int64_t)(col + cc) * cols.ldq + 16 * bm) = out;
-          s[(int64_t)(col + cc) * cols.lds + bm] = (uint8_t)sb;
-        }
-      }
+    for (int c = 0; c < 4; ++c) {
+      sb[c] = scale_byte(m[c]);
+      col_scales[(4 * lane + c) * W + wave] = (uint8_t)sb[c];
     }
+    col_codes[slot] = p.template column<0>(scale_value(sb[0]), code_mask(sb[0]));
+    col_codes[slot + W] = p.template column<1>(scale_value(sb[1]), code_mask(sb[1]));
+    col_codes[slot + 2 * W] = p.template column<2>(scale_value(sb[2]), code_mask(sb[2]));
+    col_codes[slot + 3 * W] = p.template column<3>(scale_value(sb[3]), code_mask(sb[3]));
   }
 
   // along the rows
   if constexpr (ROWS) {
     auto* q = static_cast<uint8_t*>(rows.q);
-    auto* s = static_cast<uint8_t*>(rows.s);
-    const bool live = col < (int)blocks_of(K) * BLOCK;
+    const int nb = (int)blocks_of(K), quad = lane & 3;
+    uint32_t mine = 0;  // the scales of rows 4 (lane % 8) .. + 3 of this lane's block, one byte each
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      uint32_t m;
-      uint32_t code = 0;
-      uint32_t sb;
-      if constexpr (T == FP4_TYPE_F32) {
-        m = max(max(v[i][0] & 0x7fffffffu, v[i][1] & 0x7fffffffu), max(v[i][2] & 0x7fffffffu, v[i][3] & 0x7fffffffu));
-        m = quad_max(m);
-        m = max(m, dpp<DPP_HALF_MIRROR>(m));
-        sb = scale_byte(m);
-        const float sc = scale_value(sb);
-        code = cvt_pair32<0>(code, v[i][0], v[i][1], sc);
-        code = cvt_pair32<1>(code, v[i][2], v[i][3], sc);
-        code &= code_mask(sb);
-        code |= dpp<DPP_XOR1>(code) << 16;  // the even lane of a pair stores both halves
-      } else {
-        m = max_u16x2(max_u16x2(v[i][0] & 0x7fff7fffu, v[i][1] & 0x7fff7fffu),
-                      max_u16x2(v[i][2] & 0x7fff7fffu, v[i][3] & 0x7fff7fffu));
-        sb = scale_byte(amax_bits16<T>(quad_max(max(m & 0xffffu, m >> 16))));
-        const float sc = scale_value(sb);
-        code = cvt_pair16<T, 0>(code, v[i][0], sc);
-        code = cvt_pair16<T, 1>(code, v[i][1], sc);
-        code = cvt_pair16<T, 2>(code, v[i][2], sc);
-        code = cvt_pair16<T, 3>(code, v[i][3], sc);
-        code &= code_mask(sb);
-      }
-      if (row0 + i < M && live) {
-        uint8_t* qr = q + (int64_t)(row0 + i) * rows.ldq + (col >> 1);
-        if constexpr (T == FP4_TYPE_F32) {
-          if (!(lane & 1)) *reinterpret_cast<uint32_t*>(qr) = code;
-          if (!(lane & 7)) s[(int64_t)(row0 + i) * rows.lds + (col >> 5)] = (uint8_t)sb;
-        } else {
-          *reinterpret_cast<uint32_t*>(qr) = code;
-          if (!(lane & 3)) s[(int64_t)(row0 + i) * rows.lds + (col >> 5)] = (uint8_t)sb;
-        }
-      }
+    for (int g = 0; g < 8; ++g) {
+      // four rows at a time: without this the compiler keeps the magnitudes of the column pass and every row's
+      // exchange alive at once (up to 270 registers instead of about 90)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < R; ++j) asm volatile("" : "+v"(p.v[4 * g + i][j]));
+      uint32_t sb[4], c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p.row(4 * g + i, sb[i], c[i]);
+      if ((lane & 7) == g) mine = sb[0] | sb[1] << 8 | sb[2] << 16 | sb[3] << 24;
+      // lane q of a quad takes row 4 g + q: first rows {0, 1} against {2, 3} with the lane two away, then the rows of
+      // a pair with the neighbour
+      const uint32_t lo = c[0] | c[1] << 16, hi = c[2] | c[3] << 16;
+      const uint32_t keep = quad & 2 ? hi : lo, got = dpp<DPP_XOR2>(quad & 2 ? lo : hi);
+      const uint32_t sel = quad & 1 ? 0x07060302u : 0x05040100u, other = quad & 1 ? 0x05040100u : 0x07060302u;
+      const uint32_t own = __builtin_amdgcn_perm(got, keep, sel);  // this lane's and the far lane's codes of its row
+      const uint32_t nbr = dpp<DPP_XOR1>(__builtin_amdgcn_perm(got, keep, other));
+      // halves of own: (this lane, lane ^ 2); of nbr: (lane ^ 1, lane ^ 3)
+      const uint32_t first = quad & 1 ? __builtin_amdgcn_perm(own, nbr, 0x05040100u) : __builtin_amdgcn_perm(nbr, own, 0x05040100u);
+      const uint32_t second = quad & 1 ? __builtin_amdgcn_perm(own, nbr, 0x07060302u) : __builtin_amdgcn_perm(nbr, own, 0x07060302u);
+      const u32x2 out = quad & 2 ? u32x2{second, first} : u32x2{first, second};
+      const int row = row0 + 4 * g + quad, at = (col0 >> 1) + 8 * (lane >> 2);
+      if (row < M && at < 16 * nb) *reinterpret_cast<u32x2*>(q + (int64_t)row * rows.ldq + at) = out;
     }
+    // [row][block] bytes of this wave
+#pragma unroll
+    for (int b = 0; b < 4; ++b) row_scales[wave * 256 + (4 * (lane & 7) + b) * 8 + (lane >> 3)] = (uint8_t)(mine >> (8 * b));
+  }
+  __syncthreads();
+  if constexpr (ROWS) {
+    // lane: row lane / 2, four blocks
+    const int row = row0 + (lane >> 1), blk = (col0 >> 5) + 4 * (lane & 1);
+    if (row < M && blk < (int)blocks_of(K))
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(rows.s) + (int64_t)row * rows.lds + blk) =
+          *reinterpret_cast<const uint32_t*>(row_scales + wave * 256 + lane * 4);
+  }
+  const int nbm = (int)blocks_of(M);
+  auto* q = static_cast<uint8_t*>(cols.q);
+  auto* s = static_cast<uint8_t*>(cols.s);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = i * 64 * W + threadIdx.x, c = e / W, b = e % W;
+    if (col0 + c < K && W * tm + b < nbm)
+      *reinterpret_cast<u32x4*>(q + (int64_t)(col0 + c) * cols.ldq + 16 * (W * tm + b)) = col_codes[c * W + (b ^ ((c >> 2) & (W - 1)))];
+  }
+  for (int e = threadIdx.x; e < 64 * W; e += 64 * W) {
+    const int c = e / (W / 4), b = 4 * (e % (W / 4));
+    if (col0 + c < K && W * tm + b < nbm)
+      *reinterpret_cast<uint32_t*>(s + (int64_t)(col0 + c) * cols.lds + W * tm + b) = *reinterpret_cast<const uint32_t*>(col_scales + c * W + b);
   }
 }
 
 static int launch_quantize_cols(int type, int64_t M, int64_t K, const void* x, int64_t ldx, const fp4_mx* rows,
                                 const fp4_mx& cols, hipStream_t st) {
-  const int wc = 16 * 16 / elem_bytes(type);
-  const int64_t tk = (K + wc - 1) / wc, tm = (M + 127) / 128, tiles = tk * tm;
-  if ((tiles + 3) / 4 > 0x7fffffffLL) return FP4_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)((tiles + 3) / 4));
+  const int64_t tk = (K + 255) / 256;
+  const bool tall = tk * ((M + 255) / 256) >= 2 * fp4_device_cus();
+  const int w = tall ? 8 : 4;
+  const int64_t tiles = tk * ((M + 32 * w - 1) / (32 * w));
+  if (tiles > 0x7fffffffLL) return FP4_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)tiles), block(64 * w);
   const fp4_mx r = rows ? *rows : fp4_mx{};
-#define MX_COLS(T)                                                                                                     \
-  return rows ? fp4_launch(quantize_cols_kernel<T, true>, grid, dim3(256), 0, st, x, ldx, r, cols, M, K, tk, tiles)    \
-              : fp4_launch(quantize_cols_kernel<T, false>, grid, dim3(256), 0, st, x, ldx, r, cols, M, K, tk, tiles)
-  if (type == FP4_TYPE_F32) MX_COLS(FP4_TYPE_F32);
-  if (type == FP4_TYPE_BF16) MX_COLS(FP4_TYPE_BF16);
-  MX_COLS(FP4_TYPE_F16);
+#define MX_COLS(T, W)                                                                                            \
+  return rows ? fp4_launch(quantize_cols_kernel<T, W, true>, grid, block, 0, st, x, ldx, r, cols, M, K, tk)      \
+              : fp4_launch(quantize_cols_kernel<T, W, false>, grid, block, 0, st, x, ldx, r, cols, M, K, tk)
+#define MX_COLS_W(T)       \
+  if (tall) MX_COLS(T, 8); \
+  MX_COLS(T, 4)
+  if (type == FP4_TYPE_F32) { MX_COLS_W(FP4_TYPE_F32); }
+  if (type == FP4_TYPE_BF16) { MX_COLS_W(FP4_TYPE_BF16); }
+  MX_COLS_W(FP4_TYPE_F16);
+#undef MX_COLS_W
 #undef MX_COLS
 }
 
