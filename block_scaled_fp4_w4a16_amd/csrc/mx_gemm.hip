@@ -17,23 +17,34 @@ namespace mx {
 
 constexpr int GM_STAGE_BLOCKS = 8, GM_ROW_BYTES = 128;
 
-template <int BM, int BN>
+// A BM x BN tile by WM x WN waves with NBUF stages in LDS, 2 or 4 (a stage is loaded NBUF stages ahead).
+template <int BM_, int BN_, int WM_, int WN_, int NBUF_>
 struct Tile {
-  static constexpr int TM = BM / 32, TN = BN / 32;         // 16-row tiles per wave
-  static constexpr int ROWS = BM + BN;                     // rows of both operands, A's first
-  static constexpr int CODES = ROWS * GM_ROW_BYTES;        // bytes per stage
-  static constexpr int SCALES = ROWS * 16;                 // bytes per two stages
-  static constexpr int LDS = 2 * CODES + 2 * SCALES;
-  static constexpr int SLOTS = CODES / 16 / 256;           // 16-byte direct loads per thread and stage
-  static constexpr int SSLOTS = SCALES / 16 / 256;         // the same of the scales, per two stages
-  static_assert(TN <= TM && ROWS % 256 == 0, "");
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NBUF = NBUF_;
+  static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
+  static constexpr int TM = BM / 16 / WM, TN = BN / 16 / WN;  // 16-row tiles per wave
+  static constexpr int ROWS = BM + BN;                        // rows of both operands, A's first
+  static constexpr int CODES = ROWS * GM_ROW_BYTES;           // bytes per stage
+  static constexpr int SCALES = ROWS * 16;                    // bytes per two stages
+  static constexpr int RING = NBUF * CODES + NBUF / 2 * SCALES;
+  static constexpr int STAGE = 16 * (TN * 32 + 16);           // per wave: 16 rows of 16-bit outputs on their way out
+  static constexpr int LDS = RING + WAVES * STAGE;
+  static constexpr int SLOTS = CODES / 16 / THREADS;          // 16-byte direct loads per thread and stage
+  static constexpr int SSLOTS = (ROWS + THREADS - 1) / THREADS;  // the same of the scales, per two stages
+  static constexpr int OPS = TM + TN;                         // operands of a chunk, B's first
+  static constexpr int READ_ROWS = TM > 2 ? TM * 3 / 4 : 1;   // row tiles of a chunk during which the next one's are read
+  // direct loads of a thread that may be on their way when a stage has to be there: those of the NBUF - 2 stages
+  // behind the next one (half of them bring scales too)
+  static constexpr int BEHIND = (NBUF - 2) * SLOTS + (NBUF / 2 - 1) * SSLOTS;
+  static_assert((NBUF == 2 || NBUF == 4) && BEHIND + SLOTS < 64 && BM % (8 * WAVES) == 0 && ROWS % 64 == 0, "");
 };
 
 __device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
-// Every memory operation of this wave is done, and so is every wave's of the workgroup.
-__device__ __forceinline__ void wait_all_and_meet() {
-  __builtin_amdgcn_s_waitcnt(0);
+// Every LDS read of this wave is done, and every direct load but the last N, and so are every wave's of the workgroup.
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
   asm volatile("s_barrier" ::: "memory");
 }
 
@@ -42,60 +53,64 @@ struct Sources {
   int ldqa, ldqb, ldsa, ldsb;
 };
 
-// Direct load I of one stage's codes: instruction I of wave w brings rows 8 (4 I + w) .. + 7, eight lanes a row.
+// Direct load I of one stage's codes: instruction I of wave w brings rows 8 (WAVES I + w) .. + 7, eight lanes a row.
 // `from` (128 times the stage) is part of the range-checked offset: past the operand's last byte nothing is read.
 // NOTHING lies past every operand's last byte (an operand's tile has at most 2^30 bytes).
 constexpr uint32_t NOTHING = 1u << 31;
 
-template <int BM, int BN, int I>
+template <class G, int I>
 __device__ __forceinline__ void issue_codes_part(const Sources& src, uint8_t* buf, uint32_t from, int wave, int lane) {
-  const int first = (4 * I + wave) * 8;
+  const int first = (G::WAVES * I + wave) * 8;
   const int row = first + (lane >> 3);
   const uint32_t at = from + ((lane & 7) ^ swizzle(row)) * 16;
   auto* to = (__attribute__((address_space(3))) void*)(buf + first * GM_ROW_BYTES);
-  if constexpr (32 * I < BM)
+  if constexpr (8 * G::WAVES * I < G::BM)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(src.aq, to, 16, (uint32_t)(row * src.ldqa) + at, 0, 0, 0);
   else
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(src.bq, to, 16, (uint32_t)((row - BM) * src.ldqb) + at, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src.bq, to, 16, (uint32_t)((row - G::BM) * src.ldqb) + at, 0, 0, 0);
 }
 
-template <int BM, int BN, int I0, int I1>
+template <class G, int I0, int I1>
 __device__ __forceinline__ void issue_codes(const Sources& src, uint8_t* buf, uint32_t from, int wave, int lane) {
   if constexpr (I0 < I1) {
-    issue_codes_part<BM, BN, I0>(src, buf, from, wave, lane);
-    issue_codes<BM, BN, I0 + 1, I1>(src, buf, from, wave, lane);
+    issue_codes_part<G, I0>(src, buf, from, wave, lane);
+    issue_codes<G, I0 + 1, I1>(src, buf, from, wave, lane);
   }
 }
 
 // The direct loads of two stages' scales (`from`: 16 times the group): 64 rows per instruction, dealt to the waves.
-template <int BM, int BN>
+template <class G>
 __device__ __forceinline__ void issue_scales(const Sources& src, uint8_t* buf, uint32_t from, int wave, int lane) {
-  using G = Tile<BM, BN>;
 #pragma unroll
   for (int i = 0; i < G::SSLOTS; ++i) {
-    const int first = (4 * i + wave) * 64;
+    const int first = (G::WAVES * i + wave) * 64 % G::ROWS;  // with few rows two waves bring the same ones
     const int row = first + lane;
     auto* to = (__attribute__((address_space(3))) void*)(buf + first * 16);
-    if (first < BM) __builtin_amdgcn_raw_ptr_buffer_load_lds(src.as, to, 16, (uint32_t)(row * src.ldsa) + from, 0, 0, 0);
-    else __builtin_amdgcn_raw_ptr_buffer_load_lds(src.bs, to, 16, (uint32_t)((row - BM) * src.ldsb) + from, 0, 0, 0);
+    if (first < G::BM) __builtin_amdgcn_raw_ptr_buffer_load_lds(src.as, to, 16, (uint32_t)(row * src.ldsa) + from, 0, 0, 0);
+    else __builtin_amdgcn_raw_ptr_buffer_load_lds(src.bs, to, 16, (uint32_t)((row - G::BM) * src.ldsb) + from, 0, 0, 0);
   }
 }
 
-// acc += A B^T with scale byte C of both scale registers, as fp4 mfma() but written out so that the sum stays in the
+// acc += A B^T with scale byte C of both scale registers, as mfma() but written out so that the sum stays in the
 // accumulation registers that it came from: with the compiler's builtin, whose result is a new register, a tile of
-// 256 sums per lane is copied and spilled in the loop. The s_nop covers the two wait states between a vector
-// instruction that writes an operand and the MFMA that reads it, which the compiler does not see here.
-template <int C>
+// 256 sums per lane is copied and spilled in the loop. A vector instruction that writes an operand needs two wait
+// states before the MFMA that reads it, which the compiler does not see here: FIRST, the first MFMA behind a scheduling
+// barrier, waits for them, and no operand of the MFMAs that follow it up to the next barrier is written in between.
+template <int C, bool FIRST>
 __device__ __forceinline__ void mfma_acc(f32x4& acc, const u32x4& a, uint32_t sa, const u32x4& b, uint32_t sb) {
-#define MX_MFMA(SEL)                                                                                     \
-  asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " SEL " cbsz:4 blgp:4" \
+#define MX_MFMA_(WAIT, SEL)                                                                              \
+  asm volatile(WAIT "v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " SEL " cbsz:4 blgp:4"     \
                : "+a"(acc)                                                                               \
                : "v"(a), "v"(b), "v"(sa), "v"(sb))
-  if constexpr (C == 0) MX_MFMA("op_sel:[0,0,0] op_sel_hi:[0,0,0]");
-  else if constexpr (C == 1) MX_MFMA("op_sel:[1,1,0] op_sel_hi:[0,0,0]");
-  else if constexpr (C == 2) MX_MFMA("op_sel:[0,0,0] op_sel_hi:[1,1,0]");
-  else MX_MFMA("op_sel:[1,1,0] op_sel_hi:[1,1,0]");
+#define MX_MFMA(SEL)                                 \
+  if constexpr (FIRST) MX_MFMA_("s_nop 1\n\t", SEL); \
+  else MX_MFMA_("", SEL)
+  if constexpr (C == 0) { MX_MFMA("op_sel:[0,0,0] op_sel_hi:[0,0,0]"); }
+  else if constexpr (C == 1) { MX_MFMA("op_sel:[1,1,0] op_sel_hi:[0,0,0]"); }
+  else if constexpr (C == 2) { MX_MFMA("op_sel:[0,0,0] op_sel_hi:[1,1,0]"); }
+  else { MX_MFMA("op_sel:[1,1,0] op_sel_hi:[1,1,0]"); }
 #undef MX_MFMA
+#undef MX_MFMA_
 }
 
 // Four dwords of a row's scales (four chunks of four blocks) -> byte c is block g of chunk c.
@@ -124,12 +139,12 @@ __device__ __forceinline__ void place(int id, int total, int tiles_m, int tiles_
 }
 
 // A wave's state.
-template <int BM, int BN>
+template <class G>
 struct Wave {
-  using G = Tile<BM, BN>;
   f32x4 acc[G::TM][G::TN];
-  u32x4 a[G::TM], b[2][G::TN];          // operands; B's of even chunks in b[0], of odd ones in b[1]
-  uint32_t sa[2][G::TM], sb[2][G::TN];  // scales of two groups: byte c is this lane's block of chunk c
+  u32x4 op[2][G::OPS];                  // operands (B's, then A's) of even and of odd chunks
+  u32x4 raw[G::OPS];                    // scales as read: four dwords of a row
+  uint32_t sc[2][G::OPS];               // scales of this and the next group: byte c is this lane's block of chunk c
   Sources src;
   uint8_t* lds;
   int wave, lane;
@@ -138,93 +153,145 @@ struct Wave {
   int last_group;
   uint32_t tail;              // mask of the last group's scales
 
-  __device__ __forceinline__ uint8_t* codes(int buf) const { return lds + buf * G::CODES; }
-  __device__ __forceinline__ uint8_t* scales(int buf) const { return lds + 2 * G::CODES + buf * G::SCALES; }
-  __device__ __forceinline__ u32x4 read_codes(uint32_t at, int buf, int chunk, int t) const {
-    return *reinterpret_cast<const u32x4*>(codes(buf) + (chunk ? at ^ 64u : at) + t * 16 * GM_ROW_BYTES);
+  // Stage st of group st / 2 is in buffer st % NBUF: with `ring` = group % (NBUF / 2), buffer 2 ring + st % 2.
+  __device__ __forceinline__ uint8_t* codes(int ring, int half) const { return lds + (2 * ring + half) * G::CODES; }
+  __device__ __forceinline__ uint8_t* scales(int ring) const { return lds + G::NBUF * G::CODES + ring * G::SCALES; }
+  static __device__ __forceinline__ int ring_of(int group) { return G::NBUF == 2 ? 0 : group & (G::NBUF / 2 - 1); }
+  __device__ __forceinline__ u32x4 read_codes(uint32_t at, int ring, int half, int chunk, int t) const {
+    return *reinterpret_cast<const u32x4*>(codes(ring, half) + (chunk ? at ^ 64u : at) + t * 16 * GM_ROW_BYTES);
   }
-  __device__ __forceinline__ uint32_t read_scale(uint32_t at, int group) const {
-    return pick_scales(*reinterpret_cast<const u32x4*>(scales(group & 1) + at), lane >> 4) &
-           (group == last_group ? tail : ~0u);
+  __device__ __forceinline__ u32x4 read_op(int ring, int half, int chunk, int i) const {
+    return i < G::TN ? read_codes(frag_b, ring, half, chunk, i) : read_codes(frag_a, ring, half, chunk, i - G::TN);
   }
-  template <int S>
-  __device__ __forceinline__ void read_scales(int i, int group) {
-    sa[S][i] = read_scale(scale_a + 256 * i, group);
-    if (i < G::TN) sb[S][i] = read_scale(scale_b + 256 * i, group);
+  __device__ __forceinline__ u32x4 read_raw(int ring, int i) const {
+    const uint32_t at = i < G::TN ? scale_b + 256 * i : scale_a + 256 * (i - G::TN);
+    return *reinterpret_cast<const u32x4*>(scales(ring) + at);
   }
-
-  // Row tile I's MFMAs of chunk C of a group (its scales are in set 0).
-  template <int C, int I>
-  __device__ __forceinline__ void mult() {
-#pragma unroll
-    for (int j = 0; j < G::TN; ++j) mfma_acc<C>(acc[I][j], b[C & 1][j], sb[0][j], a[I], sa[0][I]);
-  }
-  // After row tile I of chunk C: A's row tile I of the next chunk, and two of B's in the first half of the rows.
-  template <int C, int I>
-  __device__ __forceinline__ void fetch() {
-    constexpr int NC = (C + 1) & 1, NB = ((C + 1) >> 1) & 1;
-    a[I] = read_codes(frag_a, NB, NC, I);
-    if constexpr (2 * I < G::TN) b[NC][2 * I] = read_codes(frag_b, NB, NC, 2 * I);
-    if constexpr (2 * I + 1 < G::TN) b[NC][2 * I + 1] = read_codes(frag_b, NB, NC, 2 * I + 1);
+  __device__ __forceinline__ uint32_t pick(int i, int group) const {
+    return pick_scales(raw[i], lane >> 4) & (group == last_group ? tail : ~0u);
   }
 
-  // A stage's first chunk, from row tile I on.
+  // What is done between the MFMAs of row tile I of chunk C: direct loads (second chunk of a stage), reads of the next
+  // chunk's operands, reads of the next group's scales (the group's last chunk), in this order; operation X of them.
   template <int C, int I>
-  __device__ __forceinline__ void first_chunk() {
-    if constexpr (I < G::TM) {
-      mult<C, I>();
-      fetch<C, I>();
-      __builtin_amdgcn_sched_barrier(0);
-      first_chunk<C, I + 1>();
+  struct Between {
+    static constexpr bool reads = I < G::READ_ROWS;
+    static constexpr int l0 = C & 1 ? G::SLOTS * I / G::TM : 0, l1 = C & 1 ? G::SLOTS * (I + 1) / G::TM : 0;
+    static constexpr int r0 = reads ? G::OPS * I / G::READ_ROWS : 0, r1 = reads ? G::OPS * (I + 1) / G::READ_ROWS : 0;
+    static constexpr int s0 = C == 3 ? r0 : 0, s1 = C == 3 ? r1 : 0;
+    static constexpr int loads = l1 - l0, ops = r1 - r0, scales = s1 - s0, all = loads + ops + scales;
+  };
+  template <int C, int I, int X, int END>
+  __device__ __forceinline__ void between(int group, int next, uint32_t codes_from) {
+    if constexpr (X < END) {
+      using B = Between<C, I>;
+      if constexpr (X < B::loads) {
+        issue_codes_part<G, B::l0 + X>(src, codes(ring_of(group), C >> 1), codes_from, wave, lane);
+      } else if constexpr (X < B::loads + B::ops) {
+        constexpr int i = B::r0 + X - B::loads, NC = (C + 1) & 1, NH = ((C + 1) >> 1) & 1;
+        op[NC][i] = read_op(ring_of(C == 3 ? next : group), NH, NC, i);
+      } else {
+        constexpr int i = B::s0 + X - B::loads - B::ops;
+        raw[i] = read_raw(ring_of(next), i);
+      }
+      between<C, I, X + 1, END>(group, next, codes_from);
     }
   }
 
-  // A stage's second chunk, from row tile I on. After row tile 0 the stage ends; the direct loads of the stage after
-  // the next (from byte `codes_from` of the codes, `scales_from` of the scales) are spread over the rows. `group` is
-  // the group of the next stage.
-  template <int C, int I>
-  __device__ __forceinline__ void second_chunk(uint32_t codes_from, uint32_t scales_from, int group) {
+  // Chunk C of `group` (`next` is the group after it) from its MFMA (I, J) on, a share of the other work behind each. A stage's second chunk ends the
+  // stage behind its first MFMA (every LDS read of the stage was issued in the chunk before) and issues the loads of the
+  // stage NBUF behind it (from byte `codes_from` of the codes and `scales_from` of the scales), whose buffer is free.
+  template <int C, int I, int J>
+  __device__ __forceinline__ void chunk(int group, int next, uint32_t codes_from, uint32_t scales_from) {
     if constexpr (I < G::TM) {
-      mult<C, I>();
-      if constexpr (I == 0) {
-        __builtin_amdgcn_sched_barrier(0);
-        wait_all_and_meet();
+      mfma_acc<C, J == 0>(acc[I][J], op[C & 1][J], sc[0][J], op[C & 1][G::TN + I], sc[0][G::TN + I]);
+      if constexpr ((C & 1) && I == 0 && J == 0) wait_and_meet<G::BEHIND>();
+      using B = Between<C, I>;
+      if constexpr (C == 3 && J == 0 && I > 0) {  // the scales read behind the row tile before
+        using P = Between<C, I - 1>;
+#pragma unroll
+        for (int i = P::s0; i < P::s1; ++i) sc[1][i] = pick(i, next);
       }
-      fetch<C, I>();
-      if constexpr (C == 3) read_scales<1>(I, group);
-      issue_codes<BM, BN, G::SLOTS * I / G::TM, G::SLOTS*(I + 1) / G::TM>(src, codes(C >> 1), codes_from, wave, lane);
-      if constexpr (C == 1 && I == G::TM - 1) issue_scales<BM, BN>(src, scales((group + 1) & 1), scales_from, wave, lane);
+      between<C, I, B::all * J / G::TN, B::all*(J + 1) / G::TN>(group, next, codes_from);
+      if constexpr (C == 1 && I == G::TM - 1 && J == G::TN - 1) issue_scales<G>(src, scales(ring_of(group)), scales_from, wave, lane);
       __builtin_amdgcn_sched_barrier(0);
-      second_chunk<C, I + 1>(codes_from, scales_from, group);
+      chunk<C, J + 1 < G::TN ? I : I + 1, J + 1 < G::TN ? J + 1 : 0>(group, next, codes_from, scales_from);
     }
   }
 };
 
-// parts > 1: part p sums stages [p per, (p + 1) per) into plane p of `y` (FP32, M x N), else all of K into y.
-template <int BM, int BN>
-__global__ void __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2)
-    gemm_kernel(fp4_mx a, fp4_mx b, void* __restrict__ y, int64_t ldy, int M, int N, int K, int out_type, int vec, int tiles_m,
-                int tiles_n, int parts, int per) {
-  using G = Tile<BM, BN>;
+// Two FP32 sums -> two outputs of a 16-bit type in one register, rounded to nearest even.
+template <int OUT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (OUT == FP4_TYPE_BF16) return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+  else return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+}
+
+// Stores a wave's sums: acc[i][j][e] is row `row0` + 16 i (+ lane % 16), column `col0` + 16 j + 4 (lane / 16) + e. Whole
+// tiles (`full`: every row and column exists and 16-byte stores are aligned) go 16 rows at a time through `stage` (this
+// wave's LDS), so that a store instruction writes long runs of a few rows, whole lines, and not 64 bytes of each of 16
+// rows, which take several times as long to issue.
+template <int OUT, class G>
+__device__ __forceinline__ void store_tile(const f32x4 (&acc)[G::TM][G::TN], void* y, int64_t ldy, int M, int N, int row0, int col0,
+                                           int lane, bool full, bool vec, uint8_t* stage) {
+  const int n = lane & 15, g = lane >> 4;
+  if (full) {
+    constexpr int EB = elem_bytes(OUT), SPLIT = OUT == FP4_TYPE_F32 && G::TN > 1 ? 2 : 1;  // column halves of FP32
+    constexpr int TJ = G::TN / SPLIT, RUN = TJ * 16 * EB, STRIDE = RUN + 16;
+    constexpr int PER = RUN / 16, ROWS = 64 / PER;  // lanes per row and rows per store
+    uint8_t* const in = stage + n * STRIDE + 4 * g * EB;
+    const uint8_t* const out = stage + lane / PER * STRIDE + lane % PER * 16;
+    uint8_t* p = static_cast<uint8_t*>(y) + ((int64_t)(row0 + lane / PER) * ldy + col0) * EB + lane % PER * 16;
+#pragma unroll
+    for (int i = 0; i < G::TM; ++i) {
+#pragma unroll
+      for (int h = 0; h < SPLIT; ++h) {
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+          const f32x4 v = acc[i][h * TJ + j];
+          if constexpr (OUT == FP4_TYPE_F32) *reinterpret_cast<f32x4*>(in + j * 64) = v;
+          else *reinterpret_cast<u32x2*>(in + j * 32) = u32x2{pack2<OUT>(v[0], v[1]), pack2<OUT>(v[2], v[3])};
+        }
+        asm volatile("" ::: "memory");  // one wave's LDS accesses stay in order: no barrier
+#pragma unroll
+        for (int r = 0; r < 16; r += ROWS)
+          *reinterpret_cast<u32x4*>(p + (int64_t)(16 * i + r) * ldy * EB + h * RUN) = *reinterpret_cast<const u32x4*>(out + r * STRIDE);
+        asm volatile("" ::: "memory");
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < G::TM; ++i)
+#pragma unroll
+      for (int j = 0; j < G::TN; ++j) {
+        const int row = row0 + 16 * i + n, col = col0 + 16 * j + 4 * g;
+        if (row < M && col < N) store4(OUT, y, (int64_t)row * ldy + col, acc[i][j], N - col, vec);
+      }
+  }
+}
+
+// One tile's work: its first row and column, its part of K and the stages [s0, s1) of that part.
+struct Job {
+  int m0, n0, part, s0, s1;
+};
+
+// parts > 1: part p sums stages [p per, (p + 1) per) into plane p of `y` (FP32, M x N), else all of K into y. A workgroup
+// takes tiles blockIdx.x, + gridDim.x, ... as one stream of stages: behind a tile's last stages the next tile's first ones
+// are loaded, and its first operands are read, as if K went on, so that between two tiles only the sums are stored.
+template <class G, int OUT>
+__global__ void __launch_bounds__(G::THREADS, G::LDS > 80 * 1024 ? G::WAVES / 4 : G::WAVES / 2)
+    gemm_kernel(fp4_mx a, fp4_mx b, void* __restrict__ y, int64_t ldy, int M, int N, int K, int vec, int tiles_m, int tiles_n,
+                int parts, int per) {
+  constexpr int BM = G::BM, BN = G::BN, NBUF = G::NBUF;
   extern __shared__ uint8_t lds[];
-  Wave<BM, BN> w;
+  Wave<G> w;
   w.lds = lds;
   w.lane = threadIdx.x & 63;
   w.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = w.lane & 15, g = w.lane >> 4;
-  int tm, tn, part;
-  place(blockIdx.x, gridDim.x, tiles_m, tiles_n, tm, tn, part);
-  const int m0 = tm * BM, n0 = tn * BN;
   const int nb = (int)blocks_of(K), stages_all = (nb + GM_STAGE_BLOCKS - 1) / GM_STAGE_BLOCKS;
-  const int s0 = part * per, s1 = min(stages_all, s0 + per);  // s0 is even: no part begins inside a scale group
-
-  const int ma = min(M - m0, BM), mb = min(N - n0, BN);
+  const int total = tiles_m * tiles_n * parts;
   w.src.ldqa = (int)a.ldq, w.src.ldqb = (int)b.ldq, w.src.ldsa = (int)a.lds, w.src.ldsb = (int)b.lds;
-  const int sbytes = (nb + 3) & ~3;
-  w.src.aq = fp4::make_rsrc(static_cast<const uint8_t*>(a.q) + (int64_t)m0 * a.ldq, (uint32_t)((ma - 1) * (int)a.ldq + nb * 16));
-  w.src.as = fp4::make_rsrc(static_cast<const uint8_t*>(a.s) + (int64_t)m0 * a.lds, (uint32_t)((ma - 1) * (int)a.lds + sbytes));
-  w.src.bq = fp4::make_rsrc(static_cast<const uint8_t*>(b.q) + (int64_t)n0 * b.ldq, (uint32_t)((mb - 1) * (int)b.ldq + nb * 16));
-  w.src.bs = fp4::make_rsrc(static_cast<const uint8_t*>(b.s) + (int64_t)n0 * b.lds, (uint32_t)((mb - 1) * (int)b.lds + sbytes));
 
   // this lane's valid blocks of the last group of four chunks
   w.last_group = (stages_all - 1) >> 1;
@@ -233,80 +300,94 @@ __global__ void __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2)
   for (int c = 0; c < 4; ++c)
     if (16 * w.last_group + 4 * c + g < nb) w.tail |= 0xffu << (8 * c);
 
-  const int arow = (w.wave >> 1) * (BM / 2), brow = BM + (w.wave & 1) * (BN / 2);  // this wave's first rows in LDS
-  const uint32_t at = n * GM_ROW_BYTES + ((g ^ swizzle(n)) << 4);                  // (multiples of 16)
+  // this wave's first rows in LDS (multiples of 16)
+  const int arow = w.wave / G::WN * (BM / G::WM), brow = BM + w.wave % G::WN * (BN / G::WN);
+  const uint32_t at = n * GM_ROW_BYTES + ((g ^ swizzle(n)) << 4);
   w.frag_a = arow * GM_ROW_BYTES + at, w.frag_b = brow * GM_ROW_BYTES + at;
   w.scale_a = (arow + n) * 16, w.scale_b = (brow + n) * 16;
-#pragma unroll
-  for (int i = 0; i < G::TM; ++i)
-#pragma unroll
-    for (int j = 0; j < G::TN; ++j) w.acc[i][j] = f32x4{0, 0, 0, 0};
 
-  const auto codes_from = [&](int st) { return st < s1 ? (uint32_t)st * GM_ROW_BYTES : NOTHING; };
-  issue_codes<BM, BN, 0, G::SLOTS>(w.src, w.codes(0), codes_from(s0), w.wave, w.lane);
-  issue_scales<BM, BN>(w.src, w.scales((s0 >> 1) & 1), (uint32_t)(s0 >> 1) * 16, w.wave, w.lane);
-  wait_all_and_meet();
-  issue_codes<BM, BN, 0, G::SLOTS>(w.src, w.codes(1), codes_from(s0 + 1), w.wave, w.lane);
+  // tile `id`: its place, and the sources of its loads
+  const auto job_of = [&](int id) {
+    Job j;
+    int tm, tn;
+    place(id, total, tiles_m, tiles_n, tm, tn, j.part);
+    j.m0 = tm * BM, j.n0 = tn * BN;
+    j.s0 = j.part * per, j.s1 = min(stages_all, j.s0 + per);  // s0 is even: no part begins inside a scale group
+    return j;
+  };
+  const auto load_from = [&](const Job& j) {
+    const int ma = min(M - j.m0, BM), mb = min(N - j.n0, BN), sbytes = (nb + 3) & ~3;
+    w.src.aq = fp4::make_rsrc(static_cast<const uint8_t*>(a.q) + j.m0 * a.ldq, (uint32_t)((ma - 1) * (int)a.ldq + nb * 16));
+    w.src.as = fp4::make_rsrc(static_cast<const uint8_t*>(a.s) + j.m0 * a.lds, (uint32_t)((ma - 1) * (int)a.lds + sbytes));
+    w.src.bq = fp4::make_rsrc(static_cast<const uint8_t*>(b.q) + j.n0 * b.ldq, (uint32_t)((mb - 1) * (int)b.ldq + nb * 16));
+    w.src.bs = fp4::make_rsrc(static_cast<const uint8_t*>(b.s) + j.n0 * b.lds, (uint32_t)((mb - 1) * (int)b.lds + sbytes));
+  };
+  const auto codes_from = [](int st, int end) { return st < end ? (uint32_t)st * GM_ROW_BYTES : NOTHING; };
+  const auto scales_from = [](int st, int end) { return st < end ? (uint32_t)(st >> 1) * 16 : NOTHING; };
+
+  int id = blockIdx.x;
+  Job job = job_of(id);
+  load_from(job);
 #pragma unroll
-  for (int i = 0; i < G::TM; ++i) {
-    w.a[i] = w.read_codes(w.frag_a, 0, 0, i);
-    if (i < G::TN) w.b[0][i] = w.read_codes(w.frag_b, 0, 0, i);
-    w.template read_scales<0>(i, s0 >> 1);
+  for (int i = 0; i < NBUF; ++i) {
+    const int st = job.s0 + i, ring = w.ring_of(st >> 1);
+    issue_codes<G, 0, G::SLOTS>(w.src, w.codes(ring, i & 1), codes_from(st, job.s1), w.wave, w.lane);
+    if (!(i & 1)) issue_scales<G>(w.src, w.scales(ring), scales_from(st, job.s1), w.wave, w.lane);
   }
-  // Two stages (one group of scales) at a time. Past the last stage nothing is loaded: its look ahead reads what is
-  // in LDS and is not used, and the second half of an odd count multiplies by the zero scales of blocks past K. One
-  // loop body without branches serves every stage.
-  for (int st = s0; st < s1; st += 2) {
-    const int group = st >> 1;
-    w.template first_chunk<0, 0>();
-    w.template second_chunk<1, 0>(codes_from(st + 2), st + 2 < s1 ? (uint32_t)(group + 1) * 16 : NOTHING, group);
-    w.template first_chunk<2, 0>();
-    w.template second_chunk<3, 0>(codes_from(st + 3), 0, group + 1);
+  wait_and_meet<G::BEHIND + G::SLOTS>();
 #pragma unroll
-    for (int i = 0; i < G::TM; ++i) w.sa[0][i] = w.sa[1][i];
+  for (int i = 0; i < G::OPS; ++i) {
+    w.op[0][i] = w.read_op(w.ring_of(job.s0 >> 1), 0, 0, i);
+    w.raw[i] = w.read_raw(w.ring_of(job.s0 >> 1), i);
+  }
 #pragma unroll
-    for (int j = 0; j < G::TN; ++j) w.sb[0][j] = w.sb[1][j];
+  for (int i = 0; i < G::OPS; ++i) w.sc[0][i] = w.pick(i, job.s0 >> 1);
+
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < G::TM; ++i)
+#pragma unroll
+      for (int j = 0; j < G::TN; ++j) w.acc[i][j] = f32x4{0, 0, 0, 0};
+    __builtin_amdgcn_sched_barrier(0);
+    Job next = job;
+    id += gridDim.x;
+    // Two stages (one group of scales) at a time; the stages NBUF ahead are loaded. Past the workgroup's last stage
+    // nothing is: the look ahead reads what is in LDS and is not used. The second half of an odd count multiplies by
+    // the zero scales of blocks past K. One loop body without branches serves every stage.
+    for (int st = job.s0; st < job.s1; st += 2) {
+      int ahead = st + NBUF, end = job.s1, next_group = (st >> 1) + 1;
+      if (st + 2 >= job.s1) {
+        if (id < total) {  // only with NBUF = 2
+          next = job_of(id);
+          load_from(next);
+          ahead = next.s0, end = next.s1;
+        }
+        next_group = next.s0 >> 1;
+      }
+      w.template chunk<0, 0, 0>(st >> 1, next_group, 0, 0);
+      w.template chunk<1, 0, 0>(st >> 1, next_group, codes_from(ahead, end), scales_from(ahead, end));
+      w.template chunk<2, 0, 0>(st >> 1, next_group, 0, 0);
+      w.template chunk<3, 0, 0>(st >> 1, next_group, codes_from(ahead + 1, end), 0);
+#pragma unroll
+      for (int i = 0; i < G::OPS; ++i) w.sc[0][i] = w.sc[1][i];
+      __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // the last MFMAs' results: 18 wait states before anything but an MFMA reads them, then every read of a sum is
+    // ordered behind the wait
+    asm volatile("s_nop 15\n\ts_nop 15");
+#pragma unroll
+    for (int i = 0; i < G::TM; ++i)
+#pragma unroll
+      for (int j = 0; j < G::TN; ++j) asm volatile("" : "+a"(w.acc[i][j]));
+    void* const yp = parts > 1 ? static_cast<float*>(y) + (int64_t)job.part * M * ldy : y;
+    store_tile<OUT, G>(w.acc, yp, ldy, M, N, job.m0 + arow, job.n0 + brow - BM, w.lane,
+                       vec && job.m0 + BM <= M && job.n0 + BN <= N, vec, lds + G::RING + w.wave * G::STAGE);
+    if (id >= total) break;
+    job = next;
   }
   // no direct load may be on its way when the workgroup ends and its LDS goes to another
   __builtin_amdgcn_s_waitcnt(0);
-
-  // the last MFMAs' results: 18 wait states before anything but an MFMA reads them, then every read of a sum is
-  // ordered behind the wait
-  asm volatile("s_nop 15\n\ts_nop 15");
-#pragma unroll
-  for (int i = 0; i < G::TM; ++i)
-#pragma unroll
-    for (int j = 0; j < G::TN; ++j) asm volatile("" : "+a"(w.acc[i][j]));
-
-  if (parts > 1) y = static_cast<float*>(y) + (int64_t)part * M * ldy;
-  const int row0 = m0 + arow + n, col0 = n0 + brow - BM + 4 * g;
-  if (vec && m0 + BM <= M && n0 + BN <= N) {
-    if (out_type == FP4_TYPE_F32) {
-      float* p = static_cast<float*>(y) + (int64_t)row0 * ldy + col0;
-#pragma unroll
-      for (int i = 0; i < G::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < G::TN; ++j) *reinterpret_cast<f32x4*>(p + (int64_t)16 * i * ldy + 16 * j) = w.acc[i][j];
-    } else {
-      uint16_t* p = static_cast<uint16_t*>(y) + (int64_t)row0 * ldy + col0;
-#pragma unroll
-      for (int i = 0; i < G::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < G::TN; ++j) {
-          const f32x4 v = w.acc[i][j];
-          *reinterpret_cast<u32x2*>(p + (int64_t)16 * i * ldy + 16 * j) =
-              u32x2{to16(out_type, v[0]) | to16(out_type, v[1]) << 16, to16(out_type, v[2]) | to16(out_type, v[3]) << 16};
-        }
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < G::TM; ++i)
-#pragma unroll
-    for (int j = 0; j < G::TN; ++j) {
-      const int row = row0 + 16 * i, col = col0 + 16 * j;
-      if (row < M && col < N) store4(out_type, y, (int64_t)row * ldy + col, w.acc[i][j], N - col, vec);
-    }
 }
 
 // y = the sum of the K parts' planes, in the order of the parts. Planes have rows of `ldp` floats (a multiple of 4).
@@ -322,70 +403,96 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
 
 // How a product is run.
 struct Plan {
-  int rows;    // 1: rows_kernel, else gemm_kernel
-  int tile;    // 256 or 128
+  int tile;    // 0: rows_kernel, else gemm_kernel with tiles of 64, 128 or 256
   int parts;   // K parts
   int per;     // stages per part (even)
   int64_t ldp; // floats per row of a plane
 };
 
+// What a tile costs, in microseconds as measured on 256 compute units: a launch with its first loads and last stores,
+// each further round's stores, and a stage of 256 positions with one workgroup on a unit and with two (64 and 128: two
+// fit; their stages run at 16 and 28 outputs per nanosecond, those of 256 at 37).
+struct TileCost {
+  int tile;
+  double launch, round, one, two;
+};
+constexpr TileCost TILE_COSTS[] = {{64, 3.2, 0.6, 0.27, 0.5}, {128, 4.4, 1.6, 0.67, 1.15}, {256, 9.0, 4.0, 1.75, 0}};
+
+// The cheapest of the tiles and K parts by those figures. Parts (only where one round of tiles leaves units idle) cost a
+// second kernel and their planes' way to memory and back: 2.5 us and 1.2 bytes per picosecond. For example 333 x 2560,
+// K = 9728: tiles of 64 take 13.9 us, of 128 29.9 us; 64 x 2560, K = 9728: 14.2 us, in 4 parts 9.8 us.
 static Plan plan_of(int64_t M, int64_t N, int64_t K) {
   Plan p{};
   p.ldp = (N + 3) / 4 * 4;
+  const int stages = (int)((blocks_of(K) + 7) / 8), cus = fp4_device_cus();
   p.parts = 1;
-  const int stages = (int)((blocks_of(K) + 7) / 8);
   p.per = (stages + 1) & ~1;
-  if (M <= 64) {
-    p.rows = 1;
-    return p;
-  }
-  const int cus = fp4_device_cus();
-  auto tiles = [&](int t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
-  p.tile = tiles(256) >= cus ? 256 : 128;
-  const int64_t grid = tiles(p.tile);
-  if (p.tile == 128 && grid < cus && stages >= 4) {
-    int64_t want = 2 * cus / grid;
-    if (want > 16) want = 16;
-    int per = (int)((stages + want - 1) / want);
-    per = (per + 1) & ~1;
-    p.parts = (stages + per - 1) / per;
-    p.per = per;
+  if (M <= 16) return p;
+  double best = 1e30;
+  for (const TileCost& c : TILE_COSTS) {
+    const int64_t tiles = ((M + c.tile - 1) / c.tile) * ((N + c.tile - 1) / c.tile);
+    for (int want = 1; want <= 16; want *= 2) {
+      const int per = ((stages + want - 1) / want + 1) & ~1, parts = (stages + per - 1) / per;
+      if (want > 1 && (c.tile == 256 || parts != want || tiles * parts > cus)) break;
+      const int64_t work = tiles * parts, slots = (c.two > 0 ? 2 : 1) * (int64_t)cus;
+      const int64_t full = work / slots, rest = work - full * slots;
+      const double last = rest == 0 ? 0 : rest > cus ? c.two : c.one;
+      double us = c.launch + (full + (rest > 0) - 1) * c.round + per * (full * (c.two > 0 ? c.two : c.one) + last);
+      if (parts > 1) us += 2.5 + parts * M * p.ldp * 4 / 1.2e6;
+      if (us < best) {
+        best = us;
+        p.tile = c.tile, p.parts = parts, p.per = per;
+      }
+    }
   }
   return p;
 }
 
 static int64_t plane_bytes(const Plan& p, int64_t M) { return p.parts > 1 ? p.parts * M * p.ldp * 4 : 0; }
 
-template <int B>
+template <class G, int OUT>
+static int launch_tiles(const Plan& p, int M, int N, int K, const fp4_mx& a, const fp4_mx& b, void* y, int64_t ldy,
+                        hipStream_t st) {
+  static Fp4LdsLimit limit;
+  limit.ensure(reinterpret_cast<const void*>(&gemm_kernel<G, OUT>), G::LDS);
+  const int tm = (M + G::BM - 1) / G::BM, tn = (N + G::BN - 1) / G::BN;
+  const int64_t grid = (int64_t)tm * tn * p.parts;
+  if (grid > (1LL << 30)) return FP4_ERR_UNSUPPORTED;
+  const int vec = fp4_aligned(y, 16) && ldy % (OUT == FP4_TYPE_F32 ? 4 : 8) == 0;
+  // one workgroup per compute unit takes several tiles where only one fits (a multiple of the 8 XCDs, so that a
+  // workgroup's tiles stay on its XCD); smaller tiles overlap by sharing a unit
+  const int units = fp4_device_cus() & ~7;
+  const int64_t wgs = G::NBUF == 2 && G::LDS > 80 * 1024 && units > 0 && grid > units ? units : grid;
+  return fp4_launch(gemm_kernel<G, OUT>, dim3((unsigned)wgs), dim3(G::THREADS), G::LDS, st, a, b, y, ldy, M, N, K, vec, tm, tn,
+                    p.parts, p.per);
+}
+
+template <class G>
 static int launch_gemm(const Plan& p, int out_type, int M, int N, int K, const fp4_mx& a, const fp4_mx& b, void* y, int64_t ldy,
                        void* ws, hipStream_t st) {
-  using G = Tile<B, B>;
-  static Fp4LdsLimit limit;
-  limit.ensure(reinterpret_cast<const void*>(&gemm_kernel<B, B>), G::LDS);
-  const int tm = (M + B - 1) / B, tn = (N + B - 1) / B;
-  const int64_t grid = (int64_t)tm * tn * p.parts;
-  if (grid > 0x7fffffffLL) return FP4_ERR_UNSUPPORTED;
-  const int vec = fp4_aligned(y, 4 * elem_bytes(out_type)) && ldy % 4 == 0;
-  if (p.parts == 1)
-    return fp4_launch(gemm_kernel<B, B>, dim3((unsigned)grid), dim3(256), G::LDS, st, a, b, y, ldy, M, N, K, out_type, vec, tm,
-                      tn, 1, p.per);
-  if (int rc = fp4_launch(gemm_kernel<B, B>, dim3((unsigned)grid), dim3(256), G::LDS, st, a, b, ws, p.ldp, M, N, K, FP4_TYPE_F32,
-                          1, tm, tn, p.parts, p.per))
-    return rc;
-  const int64_t quads = (p.ldp >> 2) * M;
-  return fp4_launch(combine_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, st, ws, y, ldy, M, N, p.ldp, p.parts,
-                    out_type, vec);
+  if (p.parts > 1) {
+    if (int rc = launch_tiles<G, FP4_TYPE_F32>(p, M, N, K, a, b, ws, p.ldp, st)) return rc;
+    const int vec = fp4_aligned(y, 4 * elem_bytes(out_type)) && ldy % 4 == 0;
+    const int64_t quads = (p.ldp >> 2) * M;
+    return fp4_launch(combine_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, st, ws, y, ldy, M, N, p.ldp, p.parts,
+                      out_type, vec);
+  }
+  if (out_type == FP4_TYPE_F32) return launch_tiles<G, FP4_TYPE_F32>(p, M, N, K, a, b, y, ldy, st);
+  if (out_type == FP4_TYPE_BF16) return launch_tiles<G, FP4_TYPE_BF16>(p, M, N, K, a, b, y, ldy, st);
+  return launch_tiles<G, FP4_TYPE_F16>(p, M, N, K, a, b, y, ldy, st);
 }
 
 static int run_product(Plan p, int out_type, int64_t M, int64_t N, int64_t K, const fp4_mx& a, const fp4_mx& b, void* y,
                        int64_t ldy, void* ws, size_t ws_bytes, hipStream_t st) {
-  if (p.rows) return launch_rows(0, out_type, (int)M, (int)N, (int)K, nullptr, 0, &a, b, y, ldy, st);
+  if (p.tile == 0) return launch_rows(0, out_type, (int)M, (int)N, (int)K, nullptr, 0, &a, b, y, ldy, st);
   if (p.parts > 1 && (!ws || ws_bytes < (size_t)plane_bytes(p, M))) {
     p.parts = 1;
     p.per = ((int)((blocks_of(K) + 7) / 8) + 1) & ~1;
   }
-  return p.tile == 256 ? launch_gemm<256>(p, out_type, (int)M, (int)N, (int)K, a, b, y, ldy, ws, st)
-                       : launch_gemm<128>(p, out_type, (int)M, (int)N, (int)K, a, b, y, ldy, ws, st);
+  const auto launch = [&](auto fn) { return fn(p, out_type, (int)M, (int)N, (int)K, a, b, y, ldy, ws, st); };
+  if (p.tile == 256) return launch(launch_gemm<Tile<256, 256, 2, 2, 2>>);
+  if (p.tile == 128) return launch(launch_gemm<Tile<128, 128, 2, 2, 2>>);
+  return launch(launch_gemm<Tile<64, 64, 2, 2, 4>>);
 }
 
 static int check_product(int out_type, int64_t M, int64_t N, int64_t K) {
