@@ -427,8 +427,11 @@ static Plan plan_of(int64_t M, int64_t N, int64_t K) {
   const int stages = (int)((blocks_of(K) + 7) / 8), cus = fp4_device_cus();
   p.parts = 1;
   p.per = (stages + 1) & ~1;
-  if (M <= 16) return p;
+  // up to 16 rows: rows_kernel, by its chunk pairs and tiles of 16 (4096 x 4096 at M = 1 and 16: 3.6 and 4.6 us, tiles of 64
+  // 7.2; 14336 x 4096: 9.2 and 12.9 us against 7.8 and 8.1)
+  const double least = 2.5 + N * K * (17 / 32.) / 5e6;  // the weights' bytes at 5 TB/s
   double best = 1e30;
+  if (M <= 16) best = 1.8 + (double)((N + 15) / 16) * stages * (0.00046 + 0.000022 * M);
   for (const TileCost& c : TILE_COSTS) {
     const int64_t tiles = ((M + c.tile - 1) / c.tile) * ((N + c.tile - 1) / c.tile);
     for (int want = 1; want <= 16; want *= 2) {
@@ -438,6 +441,7 @@ static Plan plan_of(int64_t M, int64_t N, int64_t K) {
       const int64_t full = work / slots, rest = work - full * slots;
       const double last = rest == 0 ? 0 : rest > cus ? c.two : c.one;
       double us = c.launch + (full + (rest > 0) - 1) * c.round + per * (full * (c.two > 0 ? c.two : c.one) + last);
+      if (us < least) us = least;
       if (parts > 1) us += 2.5 + parts * M * p.ldp * 4 / 1.2e6;
       if (us < best) {
         best = us;
@@ -510,8 +514,12 @@ static int check_output(int out_type, int64_t N, const void* y, int64_t ldy) {
   return fp4_aligned(y, (uintptr_t)elem_bytes(out_type)) ? FP4_OK : FP4_ERR_ALIGN;
 }
 
-// Dense activations are quantised inside the product up to this many rows, into the workspace above it.
-constexpr int FUSED_ROWS = 16;
+// Whether dense activations are quantised inside the product, else into the workspace before it. Each workgroup of 16
+// weight rows then quantises all of them again, which pays while its rounds are few: 4096 x 4096 at M = 1 and 9 takes 4.5
+// and 5.8 us against 5.5 and 6.2 in two kernels, 9728 x 2560 6.8 against 6.7, 14336 x 4096 at M = 16 27 against 11.
+static bool fused(int64_t M, int64_t N, int64_t K) {
+  return M <= 16 && (N + 15) / 16 * ((blocks_of(K) + 7) / 8) <= 5120;
+}
 
 struct LinearSpace {
   int64_t q, s, planes;  // bytes, each a multiple of 256
@@ -545,7 +553,7 @@ extern "C" int w4a4_matmul(int out_type, int64_t M, int64_t N, int64_t K, const 
 
 extern "C" int64_t w4a4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (int rc = check_product(FP4_TYPE_F32, M, N, K)) return rc;
-  if (M <= FUSED_ROWS) return 0;
+  if (M == 0 || fused(M, N, K)) return 0;
   const LinearSpace sp = linear_space(plan_of(M, N, K), M, K);
   return sp.q + sp.s + sp.planes;
 }
@@ -563,7 +571,7 @@ extern "C" int w4a4_linear(int x_type, int out_type, int64_t M, int64_t N, int64
   if (int rc = check_output(out_type, N, y, ldy)) return rc;
   if (workspace && !fp4_aligned(workspace, 16)) return FP4_ERR_ALIGN;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (M <= FUSED_ROWS) return launch_rows(x_type, out_type, (int)M, (int)N, (int)K, x, ldx, nullptr, *b, y, ldy, st);
+  if (fused(M, N, K)) return launch_rows(x_type, out_type, (int)M, (int)N, (int)K, x, ldx, nullptr, *b, y, ldy, st);
   const Plan p = plan_of(M, N, K);
   const LinearSpace sp = linear_space(p, M, K);
   if (!workspace || workspace_bytes < (size_t)(sp.q + sp.s)) return FP4_ERR_ARG;

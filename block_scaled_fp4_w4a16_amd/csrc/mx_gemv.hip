@@ -1,7 +1,7 @@
 // MXFP4 products with few rows of activations (decode, drafted tokens, small batches):
 //   y[m][n] = sum_k A[m][k] B[n][k],  A in MXFP4 or dense and quantised on the way, B the weights in MXFP4.
 //
-// Bound by the bytes of B (17 per 32 weights). A workgroup owns 16 T rows of B and all of A; its waves split K in
+// Bound by the bytes of B (17 per 32 weights). A workgroup owns 16 rows of B and all of A; its waves split K in
 // pairs of 128-position chunks (a pair is one 128-byte line of a weight row), each lane reading 16-byte blocks of
 // codes that are MFMA operands as they stand: nothing is decoded, and the scaled matrix instruction applies the
 // block scales. The waves' sums meet in LDS in a fixed order.
@@ -63,119 +63,94 @@ __device__ __forceinline__ void quantize_block(const uint8_t* row, int k0, int K
   }
 }
 
-// XT: 0 for A in MXFP4, else the type of dense A. MB blocks of 16 rows of A, T tiles of 16 rows of B, U chunk
-// pairs in flight.
-template <int XT, int MB, int T, int U>
+// Blocks of operand rows by buffer loads: bytes past the operand come back as zeros.
+__device__ __forceinline__ u32x4 load_codes(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+}
+__device__ __forceinline__ u32x2 load_scales(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+  return __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0);
+}
+
+// XT: 0 for A in MXFP4, else the type of dense A. A wave takes the pairs wave, wave + waves, ... one after the other: loads
+// of several pairs at once, or of the next one ahead, took as long or longer at every size (the waves of a compute unit
+// cover each other), while more registers mean fewer waves. The arguments that the weights' loads need come first: they
+// are preloaded into scalar registers.
+template <int XT>
 __global__ void __launch_bounds__(64 * GV_MAX_WAVES)
-    rows_kernel(const uint8_t* __restrict__ bq, const uint8_t* __restrict__ bs, int ldq, int lds, const void* __restrict__ a,
-                const uint8_t* __restrict__ as, int64_t lda, int las, int M, int N, int K, void* __restrict__ y, int64_t ldy,
-                int out_type, int vec) {
-  extern __shared__ float red[];  // [waves][MB][T][64][4]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    rows_kernel(const uint8_t* __restrict__ bq, const uint8_t* __restrict__ bs, int N, int K, int ldq, int lds, int m_waves,
+                const void* __restrict__ a, const uint8_t* __restrict__ as, int64_t lda, int las, void* __restrict__ y,
+                int64_t ldy, int out_type, int vec) {
+  extern __shared__ f32x4 red[];  // [waves][64]
+  const int lane = threadIdx.x & 63, waves = m_waves >> 8, M = m_waves & 255;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int nb = (int)blocks_of(K), pairs = (nb + 7) >> 3;
-  const int n0 = blockIdx.x * 16 * T;
+  const int n0 = blockIdx.x * 16, rows = min(16, N - n0);
+  const auto wq = fp4::make_rsrc(bq + (int64_t)n0 * ldq, (uint32_t)((rows - 1) * ldq + nb * BLOCK_BYTES));
+  const auto ws = fp4::make_rsrc(bs + (int64_t)n0 * lds, (uint32_t)((rows - 1) * lds + ((nb + 3) & ~3)));
+  const uint32_t wq0 = n * ldq + g * BLOCK_BYTES, ws0 = n * lds;
 
-  const uint8_t* qrow[T];
-  const uint8_t* srow[T];
+  f32x4 acc = {0, 0, 0, 0};
+  for (int p = wave; p < pairs; p += waves) {
+    const u32x4 w[2] = {load_codes(wq, wq0 + p * 128), load_codes(wq, wq0 + p * 128 + 64)};
+    const u32x2 wsc = load_scales(ws, ws0 + p * 8);
+    __builtin_amdgcn_sched_barrier(0);
+    u32x4 av[2];
+    uint32_t asc[2];
+    if constexpr (XT == 0) {
+      // rows of A past M read nothing
+      const auto aq = fp4::make_rsrc(a, (uint32_t)((M - 1) * (int)lda + nb * BLOCK_BYTES));
+      const auto ar = fp4::make_rsrc(as, (uint32_t)((M - 1) * las + ((nb + 3) & ~3)));
+      const uint32_t at = n * (int)lda + g * BLOCK_BYTES + p * 128;
+      av[0] = load_codes(aq, at);
+      av[1] = load_codes(aq, at + 64);
+      const u32x2 s = load_scales(ar, n * las + p * 8);
+      asc[0] = s[0] >> (8 * g), asc[1] = s[1] >> (8 * g);
+    } else {
+      const uint8_t* row = static_cast<const uint8_t*>(a) + (int64_t)min(n, M - 1) * lda * elem_bytes(XT);
 #pragma unroll
-  for (int t = 0; t < T; ++t) {
-    const int64_t r = min(n0 + 16 * t + n, N - 1);
-    qrow[t] = bq + r * ldq;
-    srow[t] = bs + r * lds;
-  }
-  const uint8_t* arow[MB];
-  const uint8_t* asrow[MB];
+      for (int h = 0; h < 2; ++h) quantize_block<XT>(row, min(8 * p + 4 * h + g, nb - 1) * BLOCK, K, av[h], asc[h]);
+    }
 #pragma unroll
-  for (int b = 0; b < MB; ++b) {
-    const int64_t r = min(16 * b + n, M - 1);
-    arow[b] = static_cast<const uint8_t*>(a) + r * lda * (XT ? elem_bytes(XT) : 1);
-    asrow[b] = XT ? nullptr : as + r * las;
-  }
-
-  f32x4 acc[MB][T];
-#pragma unroll
-  for (int b = 0; b < MB; ++b)
-#pragma unroll
-    for (int t = 0; t < T; ++t) acc[b][t] = f32x4{0, 0, 0, 0};
-
-  for (int p0 = wave; p0 < pairs; p0 += waves * U) {
-    u32x4 w[U][2][T];
-    uint32_t ws[U][2][T];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int blk = 8 * (p0 + u * waves) + 4 * h + g;
-        const int at = min(blk, nb - 1);  // past the end: the last block again, with scale 2^-127 on both sides
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-          w[u][h][t] = *reinterpret_cast<const u32x4*>(qrow[t] + (int64_t)at * BLOCK_BYTES);
-          ws[u][h][t] = srow[t][at];
-        }
-      }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int blk = 8 * (p0 + u * waves) + 4 * h + g;
-        const int at = min(blk, nb - 1);
-#pragma unroll
-        for (int b = 0; b < MB; ++b) {
-          u32x4 av;
-          uint32_t sv;
-          if constexpr (XT != 0) {
-            quantize_block<XT>(arow[b], at * BLOCK, K, av, sv);
-          } else {
-            av = *reinterpret_cast<const u32x4*>(arow[b] + (int64_t)at * BLOCK_BYTES);
-            sv = asrow[b][at];
-          }
-          if (blk >= nb) sv = 0;
-#pragma unroll
-          for (int t = 0; t < T; ++t)
-            acc[b][t] = mfma<0, 0>(w[u][h][t], blk < nb ? ws[u][h][t] : 0u, av, sv, acc[b][t]);
-        }
-      }
+    for (int h = 0; h < 2; ++h) {
+      // a block past K: both scales 0, whose products are 36 2^-254 = 0 in FP32 whatever the codes are
+      const bool in = 8 * p + 4 * h + g < nb;
+      acc = mfma<0, 0>(w[h], in ? wsc[h] >> (8 * g) : 0u, av[h], in ? asc[h] : 0u, acc);
+    }
   }
 
-#pragma unroll
-  for (int b = 0; b < MB; ++b)
-#pragma unroll
-    for (int t = 0; t < T; ++t)
-      *reinterpret_cast<f32x4*>(red + ((size_t)(wave * MB + b) * T + t) * 256 + lane * 4) = acc[b][t];
+  red[wave * 64 + lane] = acc;
   __syncthreads();
-  for (int e = threadIdx.x; e < MB * T * 64; e += blockDim.x) {
-    f32x4 sum = *reinterpret_cast<const f32x4*>(red + (size_t)e * 4);
-    for (int v = 1; v < waves; ++v) sum += *reinterpret_cast<const f32x4*>(red + ((size_t)v * MB * T * 64 + e) * 4);
-    const int l = e & 63, bt = e >> 6, b = bt / T, t = bt % T;
-    const int m = 16 * b + (l & 15), c = n0 + 16 * t + 4 * (l >> 4);
-    if (m < M && c < N) store4(out_type, y, (int64_t)m * ldy + c, sum, N - c, vec);
+  if (threadIdx.x < 64) {
+    f32x4 sum = red[lane];
+    for (int v = 1; v < waves; ++v) sum += red[v * 64 + lane];
+    const int c = n0 + 4 * g;
+    if (n < M && c < N) store4(out_type, y, n * ldy + c, sum, N - c, vec);
   }
 }
 
-template <int XT, int MB, int T, int U>
+template <int XT>
 static int launch_variant(int waves, int out_type, int M, int N, int K, const void* x, int64_t ldx, const fp4_mx* a,
                           const fp4_mx& b, void* y, int64_t ldy, hipStream_t st) {
   const int eb = elem_bytes(out_type);
   const int vec = fp4_aligned(y, 4 * eb) && ldy % 4 == 0;
-  const dim3 grid((unsigned)((N + 16 * T - 1) / (16 * T)));
-  const size_t lds = (size_t)waves * MB * T * 1024;
-  return fp4_launch(rows_kernel<XT, MB, T, U>, grid, dim3(64 * waves), lds, st, b.q, b.s, b.ldq, b.lds, XT ? x : a->q,
-                    XT ? nullptr : a->s, XT ? ldx : a->ldq, XT ? 0 : a->lds, M, N, K, y, ldy, out_type, vec);
+  const dim3 grid((unsigned)((N + 15) / 16));
+  return fp4_launch(rows_kernel<XT>, grid, dim3(64 * waves), (size_t)waves * 1024, st, b.q, b.s, N, K, b.ldq, b.lds,
+                    M | waves << 8, XT ? x : a->q, XT ? nullptr : a->s, XT ? ldx : a->ldq, XT ? 0 : a->lds, y, ldy, out_type, vec);
 }
 
-// M <= 64; dense A (x_type != 0): M <= 16.
+// M <= 16.
 int launch_rows(int x_type, int out_type, int M, int N, int K, const void* x, int64_t ldx, const fp4_mx* a,
                 const fp4_mx& b, void* y, int64_t ldy, hipStream_t st) {
   const int pairs = (int)((blocks_of(K) + 7) / 8);
-  int waves = pairs < 8 ? pairs : 8;
-#define MX_GV(XT, MB, T, U) return launch_variant<XT, MB, T, U>(waves, out_type, M, N, K, x, ldx, a, b, y, ldy, st)
-  if (x_type == FP4_TYPE_F32) MX_GV(FP4_TYPE_F32, 1, 1, 2);
-  if (x_type == FP4_TYPE_BF16) MX_GV(FP4_TYPE_BF16, 1, 1, 2);
-  if (x_type == FP4_TYPE_F16) MX_GV(FP4_TYPE_F16, 1, 1, 2);
-  if (M <= 16) MX_GV(0, 1, 1, 2);
-  if (M <= 32) MX_GV(0, 2, 1, 2);
-  MX_GV(0, 4, 1, 2);
+  // ten waves, or one per pair: at 4096 x 4096 (16 pairs) 3.6 us, with 8 waves 3.7 and with 16 3.9; at 2560 x 9728 (38
+  // pairs) 5.3 us, 5.5 and 5.7; at 9728 x 2560 (10 pairs) 4.7 us, with 8 waves 4.9
+  const int waves = pairs < 10 ? pairs : 10;
+#define MX_GV(XT) return launch_variant<XT>(waves, out_type, M, N, K, x, ldx, a, b, y, ldy, st)
+  if (x_type == FP4_TYPE_F32) MX_GV(FP4_TYPE_F32);
+  if (x_type == FP4_TYPE_BF16) MX_GV(FP4_TYPE_BF16);
+  if (x_type == FP4_TYPE_F16) MX_GV(FP4_TYPE_F16);
+  MX_GV(0);
 #undef MX_GV
 }
 

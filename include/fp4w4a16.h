@@ -355,7 +355,7 @@ int fp4_dequant_mxfp4(int type, int64_t M, int64_t K, const fp4_mx* a, void* out
 
 /*
  * y[M][N] = A B^T with A (M rows) and B (N rows) of depth K in MXFP4; y is FP32, bf16 or FP16 (rounded once,
- * from the FP32 sum). M <= 64 streams B through a kernel that splits K inside the workgroup; larger M runs tiles
+ * from the FP32 sum). Few rows stream B through a kernel that splits K inside the workgroup; more run tiles
  * on the scaled matrix instruction, with K in parts where y has few tiles: each part writes an FP32 plane of the
  * workspace and a second kernel adds the planes in order. Deterministic. A partial sum past FP32's range
  * is an infinity and stays one, or becomes NaN where two of opposite sign meet.
