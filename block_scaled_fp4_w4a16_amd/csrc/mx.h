@@ -35,6 +35,11 @@ __device__ __forceinline__ float scale_value(uint32_t s) {
   return __builtin_bit_cast(float, s ? s << 23 : 0x00400000u);
 }
 
+// The same for a block known to be finite, in one instruction each: the exponent field less 2, held at 0; and a scale
+// operand of the conversions, which use its exponent field alone (the mantissa bit makes byte 0 a 2^-127).
+__device__ __forceinline__ uint32_t finite_scale_byte(uint32_t amax) { return __builtin_elementwise_sub_sat(amax >> 23, 2u); }
+__device__ __forceinline__ float finite_scale_value(uint32_t s) { return __builtin_bit_cast(float, s << 23 | 0x00400000u); }
+
 // Codes of a NaN block are zeros: only its scale byte says what it holds.
 __device__ __forceinline__ uint32_t code_mask(uint32_t s) { return s == 255u ? 0u : ~0u; }
 

@@ -167,23 +167,60 @@ struct Patch {
     }
     return out;
   }
-  // row i: the scale byte of its block (8 lanes) and this lane's four codes
+  // row i: the scale byte of its block (8 lanes) and this lane's four codes; FINITE: the patch has no infinity or NaN
+  template <bool FINITE>
   __device__ __forceinline__ void row(int i, uint32_t& sb, uint32_t& code) const {
     uint32_t m;
-    if constexpr (T == FP4_TYPE_F32)
+    if constexpr (T == FP4_TYPE_F32) {
       m = max(max(v[i][0] & 0x7fffffffu, v[i][1] & 0x7fffffffu), max(v[i][2] & 0x7fffffffu, v[i][3] & 0x7fffffffu));
-    else
-      m = max_u16x2(v[i][0] & 0x7fff7fffu, v[i][1] & 0x7fff7fffu), m = max(m & 0xffffu, m >> 16);
+    } else {  // the largest of the four in both halves
+      m = max_u16x2(v[i][0] & 0x7fff7fffu, v[i][1] & 0x7fff7fffu);
+      m = max_u16x2(m, __builtin_amdgcn_alignbit(m, m, 16));
+    }
     m = quad_max(m);
     m = max(m, dpp<DPP_HALF_MIRROR>(m));
-    if constexpr (T != FP4_TYPE_F32) m = amax_bits16<T>(m);
-    sb = scale_byte(m);
-    const float sc = scale_value(sb);
+    if constexpr (T == FP4_TYPE_F16) m = amax_bits16<T>(m & 0xffffu);
+    if constexpr (T == FP4_TYPE_BF16 && !FINITE) m &= 0xffff0000u;
+    sb = FINITE ? finite_scale_byte(m) : scale_byte(m);
+    const float sc = FINITE ? finite_scale_value(sb) : scale_value(sb);
     if constexpr (T == FP4_TYPE_F32) code = cvt_pair32<1>(cvt_pair32<0>(0, v[i][0], v[i][1], sc), v[i][2], v[i][3], sc);
     else code = cvt_pair16<T, 1>(cvt_pair16<T, 0>(0, v[i][0], sc), v[i][1], sc);
-    code &= code_mask(sb);
+    if constexpr (!FINITE) code &= code_mask(sb);
   }
 };
+
+// A wave's rows, four at a time (rows and blocks past the input's are not stored): their codes, and their scales into LDS
+// as [row][block] bytes.
+template <int T, bool FINITE>
+__device__ __forceinline__ void quantize_patch_rows(const Patch<T>& p, const fp4_mx& rows, uint8_t* scales, int row0, int col0, int lane,
+                                                    int M, int nb) {
+  const int quad = lane & 3, at = (col0 >> 1) + 8 * (lane >> 2);
+  const bool live = at < 16 * nb;
+  uint8_t* const q = static_cast<uint8_t*>(rows.q) + (int64_t)(row0 + quad) * rows.ldq + at;
+  uint32_t mine = 0;  // the scales of rows 4 (lane % 8) .. + 3 of this lane's block, one byte each
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    __builtin_amdgcn_sched_barrier(0);  // four rows at a time: every row's exchange at once does not fit the registers
+    uint32_t sb[4], c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p.template row<FINITE>(4 * g + i, sb[i], c[i]);
+    if ((lane & 7) == g) mine = sb[0] | sb[1] << 8 | sb[2] << 16 | sb[3] << 24;
+    // lane q of a quad takes row 4 g + q: first rows {0, 1} against {2, 3} with the lane two away, then the rows of
+    // a pair with the neighbour
+    const uint32_t lo = c[0] | c[1] << 16, hi = c[2] | c[3] << 16;
+    const uint32_t keep = quad & 2 ? hi : lo, got = dpp<DPP_XOR2>(quad & 2 ? lo : hi);
+    const uint32_t sel = quad & 1 ? 0x07060302u : 0x05040100u, other = quad & 1 ? 0x05040100u : 0x07060302u;
+    const uint32_t own = __builtin_amdgcn_perm(got, keep, sel);  // this lane's and the far lane's codes of its row
+    const uint32_t nbr = dpp<DPP_XOR1>(__builtin_amdgcn_perm(got, keep, other));
+    // halves of own: (this lane, lane ^ 2); of nbr: (lane ^ 1, lane ^ 3)
+    const uint32_t even = quad & 1 ? nbr : own, odd = quad & 1 ? own : nbr;
+    const uint32_t first = __builtin_amdgcn_perm(odd, even, 0x05040100u), second = __builtin_amdgcn_perm(odd, even, 0x07060302u);
+    const u32x2 out = quad & 2 ? u32x2{second, first} : u32x2{first, second};
+    if (live && row0 + 4 * g + quad < M) *reinterpret_cast<u32x2*>(q + (int64_t)(4 * g) * rows.ldq) = out;
+  }
+#pragma unroll
+  for (int b = 0; b < 4; ++b) scales[(4 * (lane & 7) + b) * 8 + (lane >> 3)] = (uint8_t)(mine >> (8 * b));
+}
 
 template <int T, int W, bool ROWS>
 __global__ void __launch_bounds__(64 * W) quantize_cols_kernel(const void* __restrict__ x, int64_t ldx, fp4_mx rows, fp4_mx cols,
@@ -199,15 +236,21 @@ __global__ void __launch_bounds__(64 * W) quantize_cols_kernel(const void* __res
   const int row0 = 32 * (W * tm + wave);
 
   Patch<T> p;
-  const uint8_t* base = static_cast<const uint8_t*>(x) + (int64_t)col * EB;
+  // row addresses are the wave's, columns the lane's
+  const uint8_t* base = static_cast<const uint8_t*>(x) + (int64_t)min(row0, M - 1) * ldx * EB;
+  const uint32_t off = (uint32_t)col * EB;
+  const int64_t step = ldx * EB;
+  const int last = M - 1 - row0;  // rows past the last one read it again
   if (col + 4 <= K) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      __builtin_memcpy(p.v[i], base + (int64_t)min(row0 + i, M - 1) * ldx * EB, 4 * EB);
+    for (int i = 0; i < 32; ++i) {
+      __builtin_memcpy(p.v[i], base + off, 4 * EB);
+      if (i < last) base += step;
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      const uint8_t* r = base + (int64_t)min(row0 + i, M - 1) * ldx * EB;
+      const uint8_t* r = base + off;
 #pragma unroll
       for (int j = 0; j < R; ++j) p.v[i][j] = 0;
 #pragma unroll
@@ -216,9 +259,10 @@ __global__ void __launch_bounds__(64 * W) quantize_cols_kernel(const void* __res
           if constexpr (T == FP4_TYPE_F32) p.v[i][j] = reinterpret_cast<const uint32_t*>(r)[j];
           else p.v[i][j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(r)[j] << (16 * (j & 1));
         }
+      if (i < last) base += step;
     }
   }
-  if (row0 + 32 > M) {  // rows past the last one count as zeros
+  if (row0 + 32 > M) {  // and count as zeros
 #pragma unroll
     for (int i = 0; i < 32; ++i)
 #pragma unroll
@@ -227,55 +271,30 @@ __global__ void __launch_bounds__(64 * W) quantize_cols_kernel(const void* __res
 
   // down the columns: block `wave` of column c sits in slot wave ^ (c / 4 % W) of its 16 W bytes of LDS, so that
   // neither the writes (one slot of columns 4 lane + j) nor the reads (all slots of a column) meet in a bank
-  {
-    uint32_t m[4], sb[4];
-    p.column_max(m);
-    const int slot = 4 * W * lane + (wave ^ (lane & (W - 1)));
+  uint32_t m[4], sb[4];
+  p.column_max(m);
+  // an infinity or NaN in the wave's patch shows in a column's maximum
+  const bool finite = __builtin_amdgcn_ballot_w64((max(max(m[0], m[1]), max(m[2], m[3])) >> 23) == 255u) == 0;
+  const int slot = 4 * W * lane + (wave ^ (lane & (W - 1)));
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      sb[c] = scale_byte(m[c]);
-      col_scales[(4 * lane + c) * W + wave] = (uint8_t)sb[c];
-    }
-    col_codes[slot] = p.template column<0>(scale_value(sb[0]), code_mask(sb[0]));
-    col_codes[slot + W] = p.template column<1>(scale_value(sb[1]), code_mask(sb[1]));
-    col_codes[slot + 2 * W] = p.template column<2>(scale_value(sb[2]), code_mask(sb[2]));
-    col_codes[slot + 3 * W] = p.template column<3>(scale_value(sb[3]), code_mask(sb[3]));
+  for (int c = 0; c < 4; ++c) {
+    sb[c] = scale_byte(m[c]);
+    col_scales[(4 * lane + c) * W + wave] = (uint8_t)sb[c];
   }
+  col_codes[slot] = p.template column<0>(scale_value(sb[0]), code_mask(sb[0]));
+  col_codes[slot + W] = p.template column<1>(scale_value(sb[1]), code_mask(sb[1]));
+  col_codes[slot + 2 * W] = p.template column<2>(scale_value(sb[2]), code_mask(sb[2]));
+  col_codes[slot + 3 * W] = p.template column<3>(scale_value(sb[3]), code_mask(sb[3]));
 
-  // along the rows
   if constexpr (ROWS) {
-    auto* q = static_cast<uint8_t*>(rows.q);
-    const int nb = (int)blocks_of(K), quad = lane & 3;
-    uint32_t mine = 0;  // the scales of rows 4 (lane % 8) .. + 3 of this lane's block, one byte each
+    // the column pass's magnitudes are not kept for the rows: that would double the registers
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      // four rows at a time: without this the compiler keeps the magnitudes of the column pass and every row's
-      // exchange alive at once (up to 270 registers instead of about 90)
+    for (int i = 0; i < 32; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < R; ++j) asm volatile("" : "+v"(p.v[4 * g + i][j]));
-      uint32_t sb[4], c[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) p.row(4 * g + i, sb[i], c[i]);
-      if ((lane & 7) == g) mine = sb[0] | sb[1] << 8 | sb[2] << 16 | sb[3] << 24;
-      // lane q of a quad takes row 4 g + q: first rows {0, 1} against {2, 3} with the lane two away, then the rows of
-      // a pair with the neighbour
-      const uint32_t lo = c[0] | c[1] << 16, hi = c[2] | c[3] << 16;
-      const uint32_t keep = quad & 2 ? hi : lo, got = dpp<DPP_XOR2>(quad & 2 ? lo : hi);
-      const uint32_t sel = quad & 1 ? 0x07060302u : 0x05040100u, other = quad & 1 ? 0x05040100u : 0x07060302u;
-      const uint32_t own = __builtin_amdgcn_perm(got, keep, sel);  // this lane's and the far lane's codes of its row
-      const uint32_t nbr = dpp<DPP_XOR1>(__builtin_amdgcn_perm(got, keep, other));
-      // halves of own: (this lane, lane ^ 2); of nbr: (lane ^ 1, lane ^ 3)
-      const uint32_t first = quad & 1 ? __builtin_amdgcn_perm(own, nbr, 0x05040100u) : __builtin_amdgcn_perm(nbr, own, 0x05040100u);
-      const uint32_t second = quad & 1 ? __builtin_amdgcn_perm(own, nbr, 0x07060302u) : __builtin_amdgcn_perm(nbr, own, 0x07060302u);
-      const u32x2 out = quad & 2 ? u32x2{second, first} : u32x2{first, second};
-      const int row = row0 + 4 * g + quad, at = (col0 >> 1) + 8 * (lane >> 2);
-      if (row < M && at < 16 * nb) *reinterpret_cast<u32x2*>(q + (int64_t)row * rows.ldq + at) = out;
-    }
-    // [row][block] bytes of this wave
-#pragma unroll
-    for (int b = 0; b < 4; ++b) row_scales[wave * 256 + (4 * (lane & 7) + b) * 8 + (lane >> 3)] = (uint8_t)(mine >> (8 * b));
+      for (int j = 0; j < R; ++j) asm volatile("" : "+v"(p.v[i][j]));
+    uint8_t* const s = row_scales + wave * 256;
+    if (finite) quantize_patch_rows<T, true>(p, rows, s, row0, col0, lane, M, (int)blocks_of(K));
+    else quantize_patch_rows<T, false>(p, rows, s, row0, col0, lane, M, (int)blocks_of(K));
   }
   __syncthreads();
   if constexpr (ROWS) {
