@@ -407,46 +407,62 @@ struct Plan {
   int parts;   // K parts
   int per;     // stages per part (even)
   int64_t ldp; // floats per row of a plane
+  int64_t first_n;  // > 0: columns [0, first_n) in tiles of 256, the others as a product of their own
+  double us;   // what it is taken to cost
 };
 
 // What a tile costs, in microseconds as measured on 256 compute units: a launch with its first loads and last stores,
-// each further round's stores, and a stage of 256 positions with one workgroup on a unit and with two (64 and 128: two
-// fit; their stages run at 16 and 28 outputs per nanosecond, those of 256 at 37).
+// each further round's stores, and a stage of 256 positions with one workgroup on a unit (256: with every unit busy; a
+// few workgroups of 256 run a stage in 1.2) and with two (64 and 128: two fit; their stages run at 16 and 28 outputs per
+// nanosecond, those of 256 at 37).
 struct TileCost {
   int tile;
   double launch, round, one, two;
 };
 constexpr TileCost TILE_COSTS[] = {{64, 3.2, 0.6, 0.27, 0.5}, {128, 4.4, 1.6, 0.67, 1.15}, {256, 9.0, 4.0, 1.75, 0}};
 
+static double tiles_us(const TileCost& c, int64_t work, int stages, int cus) {
+  const int64_t slots = (c.two > 0 ? 2 : 1) * (int64_t)cus, full = work / slots, rest = work - full * slots;
+  double last = rest > cus ? c.two : c.one;
+  if (c.two == 0) last = 1.2 + (c.one - 1.2) * rest / cus;
+  return c.launch + (full + (rest > 0) - 1) * c.round + stages * (full * (c.two > 0 ? c.two : c.one) + (rest > 0 ? last : 0));
+}
+
 // The cheapest of the tiles and K parts by those figures. Parts (only where one round of tiles leaves units idle) cost a
 // second kernel and their planes' way to memory and back: 2.5 us and 1.2 bytes per picosecond. For example 333 x 2560,
 // K = 9728: tiles of 64 take 13.9 us, of 128 29.9 us; 64 x 2560, K = 9728: 14.2 us, in 4 parts 9.8 us.
-static Plan plan_of(int64_t M, int64_t N, int64_t K) {
+// Where the last round of tiles of 256 would be a small one (split), the columns that fill whole rounds are one product and
+// the others a second in tiles that fill the device.
+static Plan plan_of(int64_t M, int64_t N, int64_t K, bool split = true) {
   Plan p{};
   p.ldp = (N + 3) / 4 * 4;
   const int stages = (int)((blocks_of(K) + 7) / 8), cus = fp4_device_cus();
   p.parts = 1;
   p.per = (stages + 1) & ~1;
+  p.us = 1e30;
   // up to 16 rows: rows_kernel, by its chunk pairs and tiles of 16 (4096 x 4096 at M = 1 and 16: 3.6 and 4.6 us, tiles of 64
   // 7.2; 14336 x 4096: 9.2 and 12.9 us against 7.8 and 8.1)
+  if (M <= 16) p.us = 1.8 + (double)((N + 15) / 16) * stages * (0.00046 + 0.000022 * M);
   const double least = 2.5 + N * K * (17 / 32.) / 5e6;  // the weights' bytes at 5 TB/s
-  double best = 1e30;
-  if (M <= 16) best = 1.8 + (double)((N + 15) / 16) * stages * (0.00046 + 0.000022 * M);
   for (const TileCost& c : TILE_COSTS) {
     const int64_t tiles = ((M + c.tile - 1) / c.tile) * ((N + c.tile - 1) / c.tile);
     for (int want = 1; want <= 16; want *= 2) {
       const int per = ((stages + want - 1) / want + 1) & ~1, parts = (stages + per - 1) / per;
       if (want > 1 && (c.tile == 256 || parts != want || tiles * parts > cus)) break;
-      const int64_t work = tiles * parts, slots = (c.two > 0 ? 2 : 1) * (int64_t)cus;
-      const int64_t full = work / slots, rest = work - full * slots;
-      const double last = rest == 0 ? 0 : rest > cus ? c.two : c.one;
-      double us = c.launch + (full + (rest > 0) - 1) * c.round + per * (full * (c.two > 0 ? c.two : c.one) + last);
+      double us = tiles_us(c, tiles * parts, per, cus);
       if (us < least) us = least;
       if (parts > 1) us += 2.5 + parts * M * p.ldp * 4 / 1.2e6;
-      if (us < best) {
-        best = us;
-        p.tile = c.tile, p.parts = parts, p.per = per;
-      }
+      if (us < p.us) p.us = us, p.tile = c.tile, p.parts = parts, p.per = per;
+    }
+  }
+  if (split) {
+    const TileCost& c = TILE_COSTS[2];
+    const int64_t down = (M + 255) / 256, across = (N + 255) / 256, fit = down * across / cus * cus / down;
+    if (fit > 0 && fit < across) {
+      const Plan rest = plan_of(M, N - fit * 256, K, false);
+      const double us = tiles_us(c, down * fit, (stages + 1) & ~1, cus) + rest.us;
+      if (rest.parts == 1 && us < 0.95 * p.us)
+        p.us = us, p.tile = 256, p.parts = 1, p.per = (stages + 1) & ~1, p.first_n = fit * 256;
     }
   }
   return p;
@@ -492,6 +508,14 @@ static int run_product(Plan p, int out_type, int64_t M, int64_t N, int64_t K, co
   if (p.parts > 1 && (!ws || ws_bytes < (size_t)plane_bytes(p, M))) {
     p.parts = 1;
     p.per = ((int)((blocks_of(K) + 7) / 8) + 1) & ~1;
+  }
+  if (p.first_n > 0) {
+    const int64_t n = p.first_n;
+    p.first_n = 0;
+    if (int rc = run_product(p, out_type, M, n, K, a, b, y, ldy, nullptr, 0, st)) return rc;
+    const fp4_mx rest = {static_cast<uint8_t*>(b.q) + n * b.ldq, static_cast<uint8_t*>(b.s) + n * b.lds, b.ldq, b.lds};
+    return run_product(plan_of(M, N - n, K, false), out_type, M, N - n, K, a, rest,
+                       static_cast<uint8_t*>(y) + n * elem_bytes(out_type), ldy, nullptr, 0, st);
   }
   const auto launch = [&](auto fn) { return fn(p, out_type, (int)M, (int)N, (int)K, a, b, y, ldy, ws, st); };
   if (p.tile == 256) return launch(launch_gemm<Tile<256, 256, 2, 2, 2>>);

@@ -223,7 +223,8 @@ def test_product(m, n, k):
     close(y, ref, mag, k, "no workspace")
 
 
-@pytest.mark.parametrize("m,n,k", [(4096, 4096, 320), (4095, 4097, 544), (4100, 5000, 32), (2048, 9728, 2560)])
+@pytest.mark.parametrize("m,n,k", [(4096, 4096, 320), (4095, 4097, 544), (4100, 5000, 32), (2048, 9728, 2560),
+                                   (4096, 4608, 4096), (4090, 4601, 4100)])
 def test_product_large_tiles(m, n, k):
     a = dense(m, k, torch.bfloat16, 12).cuda()
     b = dense(n, k, torch.bfloat16, 13).cuda()
