@@ -488,31 +488,17 @@ class MXTensor:
         return MXTensor(q, s, rows, k), MXTensor(qt, st, k, rows)
 
     def dequant(self, dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
-        out = torch.empty(self.rows, self.K, dtype=dtype, device=self.codes.device)
-        _native.dequant(self.rows, self.K, self.codes, self.scales, out, stream)
-        return out
+        return _native.dequant_new(self.codes, self.scales, self.rows, self.K, dtype, stream)
 
     def matmul(self, x, out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
                stream=None, workspace: torch.Tensor | None = None) -> torch.Tensor:
         """x self^T [M, rows], self the weights: x an MXTensor of the same K, or dense [M, K], quantised on the way."""
-        packed = isinstance(x, MXTensor)
-        if packed:
-            m, k = x.rows, x.K
-        else:
-            if x.dim() != 2:
-                raise ValueError("x must be [M, K] with the weights' K")
-            m, k = x.shape
-        if k != self.K:
-            raise ValueError(f"depths differ: {k} and {self.K}")
-        if out is None:
-            out = torch.empty(m, self.rows, dtype=out_dtype, device=self.codes.device)
-        if packed:
-            _native.matmul(m, self.rows, k, x.codes, x.scales, self.codes, self.scales, out, stream, workspace)
-        else:
-            if x.stride(1) != 1 and k > 1 or m > 1 and x.stride(0) < k:
-                x = x.contiguous()
-            _native.linear(m, self.rows, k, x, self.codes, self.scales, out, stream, workspace)
-        return out
+        if isinstance(x, MXTensor):
+            if x.K != self.K:
+                raise ValueError(f"depths differ: {x.K} and {self.K}")
+            return _native.matmul_new(x.codes, x.scales, x.rows, self.codes, self.scales, self.rows, self.K, out, out_dtype,
+                                      stream, workspace)
+        return _native.linear_new(x, self.codes, self.scales, self.rows, self.K, out, out_dtype, stream, workspace)
 
 
 def mx_linear(x: torch.Tensor, w: torch.Tensor) -> torch.Tensor:

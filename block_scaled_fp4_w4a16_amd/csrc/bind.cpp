@@ -219,6 +219,34 @@ void linear(int64_t M, int64_t N, int64_t K, const Tensor& x, const Tensor& bq, 
   linear_into(M, N, K, x, {bq, bs}, y, stream_of(stream, d), ws, d);
 }
 
+// The MXTensor methods: the output is allocated here unless it is given.
+Tensor output_of(const OptTensor& out, int64_t rows, int64_t cols, at::ScalarType dtype, c10::Device d) {
+  return out ? *out : at::empty({rows, cols}, at::TensorOptions().dtype(dtype).device(d));
+}
+
+Tensor dequant_new(const Tensor& codes, const Tensor& scales, int64_t rows, int64_t K, at::ScalarType dtype,
+                   const py::object& stream) {
+  Tensor out = output_of({}, rows, K, dtype, codes.device());
+  dequant(rows, K, codes, scales, out, stream);
+  return out;
+}
+
+Tensor matmul_new(const Tensor& aq, const Tensor& as, int64_t M, const Tensor& bq, const Tensor& bs, int64_t N, int64_t K,
+                  const OptTensor& out, at::ScalarType dtype, const py::object& stream, const OptTensor& ws) {
+  Tensor y = output_of(out, M, N, dtype, bq.device());
+  matmul(M, N, K, aq, as, bq, bs, y, stream, ws);
+  return y;
+}
+
+Tensor linear_new(const Tensor& x, const Tensor& bq, const Tensor& bs, int64_t N, int64_t K, const OptTensor& out,
+                  at::ScalarType dtype, const py::object& stream, const OptTensor& ws) {
+  if (x.dim() != 2) value_error("x must be [M, K] with the weights' K");
+  if (x.size(1) != K) value_error("depths differ: ", x.size(1), " and ", K);
+  Tensor y = output_of(out, x.size(0), N, dtype, bq.device());
+  linear(x.size(0), N, K, as_rows(x), bq, bs, y, stream, ws);
+  return y;
+}
+
 // Codes and scales used as they are where their rows are aligned (16 and 4 bytes), else copied.
 py::tuple from_canonical(const Tensor& codes, const Tensor& scales, std::optional<int64_t> K) {
   if (codes.scalar_type() != at::kByte || scales.scalar_type() != at::kByte) type_error("codes and scales must be uint8");
@@ -321,6 +349,9 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
   m.def("dequant", &dequant);
   m.def("matmul", &matmul);
   m.def("linear", &linear);
+  m.def("dequant_new", &dequant_new);
+  m.def("matmul_new", &matmul_new);
+  m.def("linear_new", &linear_new);
   m.def("from_canonical", &from_canonical);
   m.def("mx_linear", &mx_linear);
 }
