@@ -449,7 +449,11 @@ def w4a4_linear(M, N, K, x, bq, bs, y, stream=None, workspace=None):
 
 @dataclass
 class MXTensor:
-    """An MXFP4 operand: `rows` rows of `K` values, blocks of 32 along K (the last one padded with zeros)."""
+    """An MXFP4 operand: `rows` rows of `K` values, blocks of 32 along K (the last one padded with zeros).
+
+    A `stream` given to a method (a torch stream or a raw handle; None: the current one) takes the place of the current
+    stream for the whole call, its copies and allocations included: inputs have to be ready on it, and a result made for
+    it is used elsewhere as any tensor made under `torch.cuda.stream(stream)`."""
     codes: torch.Tensor      # uint8 [rows, 16 ceil(K / 32)], element 2j in the low half of byte j
     scales: torch.Tensor     # uint8 [rows, ceil(K / 32)], E8M0; rows a multiple of 4 bytes apart
     rows: int
@@ -506,5 +510,8 @@ def mx_linear(x: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
 
     Rounding to MXFP4 counts as the identity in the backward pass, whose products are MXFP4 too: with g the gradient of
     the result, dx = Q(g) Q(w^T)^T in x's type and dw = Q(g^T) Q(x^T)^T in w's, every operand quantised along the axis that
-    its product contracts. x and w are float32, bfloat16 or float16 on one GPU."""
+    its product contracts. x and w are float32, bfloat16 or float16 on one GPU.
+
+    A step captured into a graph takes its gradients with torch.autograd.grad; torch's accumulation into `.grad` joins the
+    stream on which an eager step that is still alive first used the leaf, which a capture cannot do."""
     return _native.mx_linear(x, w)

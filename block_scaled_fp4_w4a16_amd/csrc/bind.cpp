@@ -71,25 +71,33 @@ void check(int64_t rc, const char* what) {
   if (rc < 0) throw std::runtime_error(c10::str(what, ": ", fp4_status_string((int)rc), " (status ", rc, ")"));
 }
 
-// The caller's stream: None (the device's current one), a torch stream or a raw handle.
-struct Stream {
-  void* raw;
-  bool given;
+void* current(c10::Device d) { return c10::hip::getCurrentHIPStream(d.index()).stream(); }
+
+// Makes the caller's stream (a torch stream or a raw handle; None: leaves it alone) the device's current one for the length
+// of a call, so that the copies, outputs and workspaces the call makes are in the stream's order too.
+struct OnStream {
+  std::optional<c10::hip::HIPStream> before;
+  OnStream(const py::handle& stream, c10::Device d) {
+    if (stream.is_none()) return;
+    const py::object h =
+        py::hasattr(stream, "cuda_stream") ? py::object(stream.attr("cuda_stream")) : py::reinterpret_borrow<py::object>(stream);
+    const auto raw = reinterpret_cast<hipStream_t>(h.cast<uintptr_t>());
+    before = c10::hip::getCurrentHIPStream(d.index());
+    c10::hip::setCurrentHIPStream(c10::hip::getStreamFromExternal(raw, d.index()));
+  }
+  OnStream(const OnStream&) = delete;
+  ~OnStream() {
+    if (before) c10::hip::setCurrentHIPStream(*before);
+  }
 };
-Stream stream_of(const py::handle& stream, c10::Device d) {
-  if (stream.is_none()) return {c10::hip::getCurrentHIPStream(d.index()).stream(), false};
-  const py::object h = py::hasattr(stream, "cuda_stream") ? py::object(stream.attr("cuda_stream")) : py::reinterpret_borrow<py::object>(stream);
-  return {reinterpret_cast<void*>(h.cast<uintptr_t>()), true};
-}
-Stream current(c10::Device d) { return {c10::hip::getCurrentHIPStream(d.index()).stream(), false}; }
 
 struct Workspace {
   Tensor hold;
   void* p = nullptr;
   size_t bytes = 0;
 };
-// The given workspace, or one of `need` bytes from torch's allocator, kept from reuse until `st` is done with it.
-Workspace workspace_of(const OptTensor& given, int64_t need, c10::Device d, const Stream& st) {
+// The given workspace, or one of `need` bytes from torch's allocator.
+Workspace workspace_of(const OptTensor& given, int64_t need, c10::Device d) {
   Workspace w;
   if (given) {
     if (given->device() != d) value_error("the workspace must live on the tensors' GPU");
@@ -97,10 +105,6 @@ Workspace workspace_of(const OptTensor& given, int64_t need, c10::Device d, cons
     w.hold = *given;
   } else if (need > 0) {
     w.hold = at::empty({need}, at::TensorOptions().dtype(at::kByte).device(d));
-    if (st.given) {
-      const c10::StreamId id = c10::hip::getStreamFromExternal((hipStream_t)st.raw, d.index()).id();
-      w.hold.record_stream(c10::Stream(c10::Stream::UNSAFE, d, id));
-    }
   } else {
     return w;
   }
@@ -112,14 +116,14 @@ Workspace workspace_of(const OptTensor& given, int64_t need, c10::Device d, cons
 // ------------------------------------------------------------------------------------------------ operators
 
 void quantize_into(int64_t M, int64_t K, const Tensor& x, const Tensor* q, const Tensor* s, const Tensor* qt, const Tensor* st_,
-                   const Stream& st, c10::Device d) {
+                   c10::Device d) {
   const int type = dense_type(x, "x");
   const int64_t ldx = rows_of(x, M, K, "x");
   fp4_mx rows{}, cols{};
   if (q) rows = operand(*q, *s, M, K, "rows");
   if (qt) cols = operand(*qt, *st_, K, M, "columns");
   c10::DeviceGuard guard(d);
-  check(fp4_quantize_mxfp4(type, M, K, x.data_ptr(), ldx, q ? &rows : nullptr, qt ? &cols : nullptr, st.raw),
+  check(fp4_quantize_mxfp4(type, M, K, x.data_ptr(), ldx, q ? &rows : nullptr, qt ? &cols : nullptr, current(d)),
         "fp4_quantize_mxfp4");
 }
 
@@ -129,8 +133,8 @@ void quantize(int64_t M, int64_t K, const Tensor& x, const OptTensor& q, const O
   if (q.has_value() != s.has_value() || qt.has_value() != st_.has_value()) value_error("codes and scales come in pairs");
   rows_of(x, M, K, "x");
   const c10::Device d = one_device({&x, q ? &*q : &x, s ? &*s : &x, qt ? &*qt : &x, st_ ? &*st_ : &x});
-  quantize_into(M, K, x, q ? &*q : nullptr, s ? &*s : nullptr, qt ? &*qt : nullptr, st_ ? &*st_ : nullptr,
-                stream_of(stream, d), d);
+  const OnStream on(stream, d);
+  quantize_into(M, K, x, q ? &*q : nullptr, s ? &*s : nullptr, qt ? &*qt : nullptr, st_ ? &*st_ : nullptr, d);
 }
 
 struct Operand {
@@ -156,12 +160,12 @@ Tensor as_rows(const Tensor& x) {
 
 using Quantized = std::pair<Operand, Operand>;
 
-Quantized quantize_new(const Tensor& m, bool rows, bool cols, const Stream& st, c10::Device d) {
+Quantized quantize_new(const Tensor& m, bool rows, bool cols, c10::Device d) {
   Quantized r;
   if (rows) r.first = new_operand(m.size(0), m.size(1), d);
   if (cols) r.second = new_operand(m.size(1), m.size(0), d);
   quantize_into(m.size(0), m.size(1), m, rows ? &r.first.codes : nullptr, rows ? &r.first.scales : nullptr,
-                cols ? &r.second.codes : nullptr, cols ? &r.second.scales : nullptr, st, d);
+                cols ? &r.second.codes : nullptr, cols ? &r.second.scales : nullptr, d);
   return r;
 }
 
@@ -169,8 +173,9 @@ Quantized quantize_new(const Tensor& m, bool rows, bool cols, const Stream& st, 
 py::tuple quantize_py(const Tensor& x, bool rows, bool cols, const py::object& stream) {
   dense_type(x, "x");
   const c10::Device d = one_device({&x});
+  const OnStream on(stream, d);
   const Tensor m = as_rows(x);
-  const Quantized r = quantize_new(m, rows, cols, stream_of(stream, d), d);
+  const Quantized r = quantize_new(m, rows, cols, d);
   return py::make_tuple(m.size(0), m.size(1), r.first.codes, r.first.scales, r.second.codes, r.second.scales);
 }
 
@@ -179,11 +184,12 @@ void dequant(int64_t M, int64_t K, const Tensor& q, const Tensor& s, const Tenso
   const int64_t ldo = rows_of(out, M, K, "out");
   const c10::Device d = one_device({&q, &s, &out});
   const fp4_mx a = operand(q, s, M, K, "operand");
+  const OnStream on(stream, d);
   c10::DeviceGuard guard(d);
-  check(fp4_dequant_mxfp4(type, M, K, &a, out.data_ptr(), ldo, stream_of(stream, d).raw), "fp4_dequant_mxfp4");
+  check(fp4_dequant_mxfp4(type, M, K, &a, out.data_ptr(), ldo, current(d)), "fp4_dequant_mxfp4");
 }
 
-void matmul_into(int64_t M, int64_t N, int64_t K, const Operand& A, const Operand& B, const Tensor& y, const Stream& st,
+void matmul_into(int64_t M, int64_t N, int64_t K, const Operand& A, const Operand& B, const Tensor& y,
                  const OptTensor& ws, c10::Device d) {
   const int type = dense_type(y, "y");
   const int64_t ldy = rows_of(y, M, N, "y");
@@ -191,17 +197,18 @@ void matmul_into(int64_t M, int64_t N, int64_t K, const Operand& A, const Operan
   c10::DeviceGuard guard(d);
   const int64_t need = ws ? 0 : w4a4_matmul_workspace_bytes(M, N, K);
   check(need, "w4a4_matmul");
-  const Workspace w = workspace_of(ws, need, d, st);
-  check(w4a4_matmul(type, M, N, K, &a, &b, y.data_ptr(), ldy, w.p, w.bytes, st.raw), "w4a4_matmul");
+  const Workspace w = workspace_of(ws, need, d);
+  check(w4a4_matmul(type, M, N, K, &a, &b, y.data_ptr(), ldy, w.p, w.bytes, current(d)), "w4a4_matmul");
 }
 
 void matmul(int64_t M, int64_t N, int64_t K, const Tensor& aq, const Tensor& as, const Tensor& bq, const Tensor& bs,
             const Tensor& y, const py::object& stream, const OptTensor& ws) {
   const c10::Device d = one_device({&aq, &as, &bq, &bs, &y});
-  matmul_into(M, N, K, {aq, as}, {bq, bs}, y, stream_of(stream, d), ws, d);
+  const OnStream on(stream, d);
+  matmul_into(M, N, K, {aq, as}, {bq, bs}, y, ws, d);
 }
 
-void linear_into(int64_t M, int64_t N, int64_t K, const Tensor& x, const Operand& B, const Tensor& y, const Stream& st,
+void linear_into(int64_t M, int64_t N, int64_t K, const Tensor& x, const Operand& B, const Tensor& y,
                  const OptTensor& ws, c10::Device d) {
   const int tx = dense_type(x, "x"), ty = dense_type(y, "y");
   const int64_t ldx = rows_of(x, M, K, "x"), ldy = rows_of(y, M, N, "y");
@@ -209,14 +216,15 @@ void linear_into(int64_t M, int64_t N, int64_t K, const Tensor& x, const Operand
   c10::DeviceGuard guard(d);
   const int64_t need = ws ? 0 : w4a4_linear_workspace_bytes(M, N, K);
   check(need, "w4a4_linear");
-  const Workspace w = workspace_of(ws, need, d, st);
-  check(w4a4_linear(tx, ty, M, N, K, x.data_ptr(), ldx, &b, y.data_ptr(), ldy, w.p, w.bytes, st.raw), "w4a4_linear");
+  const Workspace w = workspace_of(ws, need, d);
+  check(w4a4_linear(tx, ty, M, N, K, x.data_ptr(), ldx, &b, y.data_ptr(), ldy, w.p, w.bytes, current(d)), "w4a4_linear");
 }
 
 void linear(int64_t M, int64_t N, int64_t K, const Tensor& x, const Tensor& bq, const Tensor& bs, const Tensor& y,
             const py::object& stream, const OptTensor& ws) {
   const c10::Device d = one_device({&x, &bq, &bs, &y});
-  linear_into(M, N, K, x, {bq, bs}, y, stream_of(stream, d), ws, d);
+  const OnStream on(stream, d);
+  linear_into(M, N, K, x, {bq, bs}, y, ws, d);
 }
 
 // The MXTensor methods: the output is allocated here unless it is given.
@@ -226,15 +234,17 @@ Tensor output_of(const OptTensor& out, int64_t rows, int64_t cols, at::ScalarTyp
 
 Tensor dequant_new(const Tensor& codes, const Tensor& scales, int64_t rows, int64_t K, at::ScalarType dtype,
                    const py::object& stream) {
+  const OnStream on(stream, one_device({&codes, &scales}));
   Tensor out = output_of({}, rows, K, dtype, codes.device());
-  dequant(rows, K, codes, scales, out, stream);
+  dequant(rows, K, codes, scales, out, py::none());
   return out;
 }
 
 Tensor matmul_new(const Tensor& aq, const Tensor& as, int64_t M, const Tensor& bq, const Tensor& bs, int64_t N, int64_t K,
                   const OptTensor& out, at::ScalarType dtype, const py::object& stream, const OptTensor& ws) {
+  const OnStream on(stream, one_device({&bq, &bs}));
   Tensor y = output_of(out, M, N, dtype, bq.device());
-  matmul(M, N, K, aq, as, bq, bs, y, stream, ws);
+  matmul(M, N, K, aq, as, bq, bs, y, py::none(), ws);
   return y;
 }
 
@@ -242,8 +252,9 @@ Tensor linear_new(const Tensor& x, const Tensor& bq, const Tensor& bs, int64_t N
                   at::ScalarType dtype, const py::object& stream, const OptTensor& ws) {
   if (x.dim() != 2) value_error("x must be [M, K] with the weights' K");
   if (x.size(1) != K) value_error("depths differ: ", x.size(1), " and ", K);
+  const OnStream on(stream, one_device({&x, &bq, &bs}));
   Tensor y = output_of(out, x.size(0), N, dtype, bq.device());
-  linear(x.size(0), N, K, as_rows(x), bq, bs, y, stream, ws);
+  linear(x.size(0), N, K, as_rows(x), bq, bs, y, py::none(), ws);
   return y;
 }
 
@@ -278,7 +289,6 @@ py::tuple from_canonical(const Tensor& codes, const Tensor& scales, std::optiona
 struct MxLinear : torch::autograd::Function<MxLinear> {
   static Tensor forward(torch::autograd::AutogradContext* ctx, const Tensor& x, const Tensor& w, bool need_dx, bool need_dw) {
     const c10::Device d = x.device();
-    const Stream st = current(d);
     const Tensor xm = as_rows(x), wm = as_rows(w);
     const int64_t m = xm.size(0), k = xm.size(1), n = wm.size(0);
     std::vector<int64_t> shape = x.sizes().vec();
@@ -286,8 +296,8 @@ struct MxLinear : torch::autograd::Function<MxLinear> {
     Tensor y = at::empty(shape, x.options().requires_grad(false).memory_format(at::MemoryFormat::Contiguous));
     Operand xt, wt;
     if (m > 0) {
-      Quantized wq = quantize_new(wm, true, need_dx, st, d), xq = quantize_new(xm, true, need_dw, st, d);
-      matmul_into(m, n, k, xq.first, wq.first, y.view({m, n}), st, {}, d);
+      Quantized wq = quantize_new(wm, true, need_dx, d), xq = quantize_new(xm, true, need_dw, d);
+      matmul_into(m, n, k, xq.first, wq.first, y.view({m, n}), {}, d);
       wt = std::move(wq.second), xt = std::move(xq.second);
     }
     ctx->save_for_backward({xt.codes, xt.scales, wt.codes, wt.scales});
@@ -310,11 +320,10 @@ struct MxLinear : torch::autograd::Function<MxLinear> {
     if (m == 0) {
       if (need_dw) dw.zero_();
     } else if (need_dx || need_dw) {
-      const Stream st = current(d);
-      const Quantized q = quantize_new(g, need_dx, need_dw, st, d);
+      const Quantized q = quantize_new(g, need_dx, need_dw, d);
       const auto saved = ctx->get_saved_variables();
-      if (need_dx) matmul_into(m, k, n, q.first, {saved[2], saved[3]}, dx.view({m, k}), st, {}, d);
-      if (need_dw) matmul_into(n, k, m, q.second, {saved[0], saved[1]}, dw, st, {}, d);
+      if (need_dx) matmul_into(m, k, n, q.first, {saved[2], saved[3]}, dx.view({m, k}), {}, d);
+      if (need_dw) matmul_into(n, k, m, q.second, {saved[0], saved[1]}, dw, {}, d);
     }
     torch::autograd::variable_list out{dx, dw, Tensor(), Tensor()};
     if (at::GradMode::is_enabled()) {  // create_graph: the gradients have no derivative, and asking for one is an error

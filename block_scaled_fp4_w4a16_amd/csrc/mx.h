@@ -156,6 +156,9 @@ static inline int check_dims(int64_t rows, int64_t k) {
   return FP4_OK;
 }
 
+// Whether a launch stays below the 2^32 work items that one can have.
+static inline bool fits_launch(int64_t workgroups, int threads) { return workgroups * threads < (1LL << 32); }
+
 // Products of already checked arguments (mx_gemv.hip, mx_gemm.hip).
 int launch_rows(int x_type, int out_type, int M, int N, int K, const void* x, int64_t ldx, const fp4_mx* a,
                 const fp4_mx& b, void* y, int64_t ldy, hipStream_t st);

@@ -477,12 +477,12 @@ static int launch_tiles(const Plan& p, int M, int N, int K, const fp4_mx& a, con
   limit.ensure(reinterpret_cast<const void*>(&gemm_kernel<G, OUT>), G::LDS);
   const int tm = (M + G::BM - 1) / G::BM, tn = (N + G::BN - 1) / G::BN;
   const int64_t grid = (int64_t)tm * tn * p.parts;
-  if (grid > (1LL << 30)) return FP4_ERR_UNSUPPORTED;
   const int vec = fp4_aligned(y, 16) && ldy % (OUT == FP4_TYPE_F32 ? 4 : 8) == 0;
   // one workgroup per compute unit takes several tiles where only one fits (a multiple of the 8 XCDs, so that a
   // workgroup's tiles stay on its XCD); smaller tiles overlap by sharing a unit
   const int units = fp4_device_cus() & ~7;
   const int64_t wgs = G::NBUF == 2 && G::LDS > 80 * 1024 && units > 0 && grid > units ? units : grid;
+  if (grid > (1LL << 30) || !fits_launch(wgs, G::THREADS)) return FP4_ERR_UNSUPPORTED;
   return fp4_launch(gemm_kernel<G, OUT>, dim3((unsigned)wgs), dim3(G::THREADS), G::LDS, st, a, b, y, ldy, M, N, K, vec, tm, tn,
                     p.parts, p.per);
 }

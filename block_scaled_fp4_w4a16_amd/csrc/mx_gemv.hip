@@ -135,6 +135,7 @@ static int launch_variant(int waves, int out_type, int M, int N, int K, const vo
   const int eb = elem_bytes(out_type);
   const int vec = fp4_aligned(y, 4 * eb) && ldy % 4 == 0;
   const dim3 grid((unsigned)((N + 15) / 16));
+  if (!fits_launch(grid.x, 64 * waves)) return FP4_ERR_UNSUPPORTED;
   return fp4_launch(rows_kernel<XT>, grid, dim3(64 * waves), (size_t)waves * 1024, st, b.q, b.s, N, K, b.ldq, b.lds,
                     M | waves << 8, XT ? x : a->q, XT ? nullptr : a->s, XT ? ldx : a->ldq, XT ? 0 : a->lds, y, ldy, out_type, vec);
 }

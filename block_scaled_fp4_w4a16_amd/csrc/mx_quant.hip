@@ -326,7 +326,7 @@ static int launch_quantize_cols(int type, int64_t M, int64_t K, const void* x, i
   const bool tall = tk * ((M + 255) / 256) >= 2 * fp4_device_cus();
   const int w = tall ? 8 : 4;
   const int64_t tiles = tk * ((M + 32 * w - 1) / (32 * w));
-  if (tiles > 0x7fffffffLL) return FP4_ERR_UNSUPPORTED;
+  if (!fits_launch(tiles, 64 * w)) return FP4_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)tiles), block(64 * w);
   const fp4_mx r = rows ? *rows : fp4_mx{};
 #define MX_COLS(T, W)                                                                                            \

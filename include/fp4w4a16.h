@@ -313,7 +313,9 @@ int fp4_quantize_q4_0(int64_t N, int64_t K, const float* w, void* blocks, void* 
  * bytes at s + r * lds. That is the layout in which MXFP4 checkpoints hold their weights, so they need no
  * repacking. ldq and q are multiples of 16, lds and s of 4. When K is not a multiple of 32 the last block's
  * codes past K are zeros (in both operands; fp4_quantize_mxfp4 writes them so). Scale bytes of a row past its
- * last block, up to the next multiple of 4, are readable and ignored. ldq, lds and K are at most 2^22.
+ * last block, up to the next multiple of 4, are readable and ignored. ldq, lds and K are at most 2^22, rows at
+ * most 2^30; what would take a launch of 2^32 work items or more (past 10^8 weight rows in a product of few rows,
+ * 2^36 outputs in small tiles) is refused with FP4_ERR_UNSUPPORTED.
  *
  * Dense tensors have a type, a row stride `ld` in elements (at least the row's length) and the alignment of
  * their element type; 16-byte aligned rows are fastest for y.

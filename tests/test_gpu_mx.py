@@ -525,6 +525,79 @@ def test_other_stream_and_given_workspace():
     assert torch.equal(b.matmul(x, workspace=ws), want)
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_given_stream_orders_copies_and_outputs(raw):
+    """Inputs that have to be copied first, on a stream that does not wait for the busy current one."""
+    m, n, k = 200, 160, 1024
+    xt = dense(k, m, torch.bfloat16, 100).cuda()
+    w = dense(n, k, torch.bfloat16, 101).cuda()
+    b = fp4.MXTensor.quantize(w)
+    want = b.matmul(xt.t().contiguous())
+    both = fp4.MXTensor.quantize_both(xt.t().contiguous())
+    wide = torch.randn(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for _ in range(4):
+            wide @ wide
+        s = side.cuda_stream if raw else side
+        y = b.matmul(xt.t(), stream=s)
+        qr, qc = fp4.MXTensor.quantize_both(xt.t(), stream=s)
+        d = qr.dequant(stream=s)
+        side.synchronize()
+        assert torch.cuda.current_stream() != side
+        got = [t.cpu() for t in (y, qr.codes, qr.scales, qc.codes, qc.scales, d)]
+        for g, e in zip(got, (want, both[0].codes, both[0].scales, both[1].codes, both[1].scales, both[0].dequant())):
+            assert torch.equal(g, e.cpu())
+
+
+def test_two_streams_at_once():
+    """Calls with workspaces of their own, interleaved on two streams from two threads."""
+    import threading
+    m, n, k = 40, 200, 8192
+    b = fp4.MXTensor.quantize(dense(n, k, torch.bfloat16, 102).cuda())
+    assert fp4.w4a4_linear_workspace_bytes(m, n, k) > 0
+    xs = [dense(m, k, torch.bfloat16, 103 + i).cuda() for i in range(2)]
+    want = [b.matmul(x) for x in xs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def run(i):
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                y = b.matmul(xs[i])
+                side.synchronize()
+                if not torch.equal(y, want[i]):
+                    bad.append(i)
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not bad
+
+
+def test_layer_with_broadcast_and_transposed_gradients():
+    """Gradients that arrive without memory of their own (a sum's) or across the rows, inputs shared by two layers."""
+    n, k = 96, 160
+    x3 = dense(5 * 14, k, torch.float32, 105).reshape(5, 14, k).transpose(0, 1).cuda()
+    w = dense(n, k, torch.float32, 106).cuda().requires_grad_()
+    x = x3.detach().requires_grad_()
+    y = fp4.mx_linear(x, w)
+    dx, dw = torch.autograd.grad(y.sum(), (x, w))
+    ex, ew = torch.autograd.grad(fp4.mx_linear(x, w), (x, w), torch.ones(14, 5, n, device="cuda"))
+    assert torch.equal(dx, ex) and torch.equal(dw, ew)
+    g = dense(n, 70, torch.float32, 107).cuda().t().reshape(14, 5, n)
+    gt = g.contiguous().transpose(0, 1).contiguous().transpose(0, 1)
+    dx, dw = torch.autograd.grad(fp4.mx_linear(x, w), (x, w), gt)
+    ex, ew = torch.autograd.grad(fp4.mx_linear(x, w), (x, w), g.contiguous())
+    assert torch.equal(dx, ex) and torch.equal(dw, ew)
+    # the same weights twice: the gradients of the two uses add
+    (d2,) = torch.autograd.grad([fp4.mx_linear(x, w), fp4.mx_linear(x, w)], w, [g, g])
+    assert torch.equal(d2, ew + ew)
+
+
 @pytest.mark.parametrize("m", [1, 9, 40, 150])
 def test_linear_in_a_graph(m):
     n, k = 200, 2048
