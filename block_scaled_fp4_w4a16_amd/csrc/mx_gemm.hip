@@ -2,9 +2,11 @@
 // entry points of the products.
 //
 // A workgroup of 4 waves (2 x 2) computes a BM x BN tile of y. Stages of 256 positions (one 128-byte line of codes
-// per row) go global -> LDS by 16-byte direct loads into two buffers; the scales of two stages (16 bytes per row)
-// travel with the even one. Each row's eight 16-byte blocks are XOR-swizzled by the row, so that the operand reads
-// (16 rows, one block each) touch every bank once. The codes are MFMA operands as they stand.
+// per row) go global -> LDS by 16-byte direct loads into a ring of buffers; the scales of two or four stages (16 or 32
+// bytes per row) travel with the first of them. Each row's eight 16-byte blocks are XOR-swizzled by the row's last three
+// bits, so that the operand reads (16 rows, one block each) are as fast as reads of consecutive bytes: 1.75 ns per
+// instruction and compute unit; with rows 8 .. 15 swizzled differently from 0 .. 7 they take 3.5. The codes are MFMA
+// operands as they stand.
 // A wave holds one chunk's operands of both matrices and the next chunk's of B: after the MFMAs of row tile i it
 // reads row tile i of the next chunk into the registers just freed, so an operand is read about a chunk ahead. In a
 // stage's second chunk every LDS read of the stage has been issued, so the barrier that ends the stage stands at
@@ -17,29 +19,32 @@ namespace mx {
 
 constexpr int GM_STAGE_BLOCKS = 8, GM_ROW_BYTES = 128;
 
-// A BM x BN tile by WM x WN waves with NBUF stages in LDS, 2 or 4 (a stage is loaded NBUF stages ahead).
-template <int BM_, int BN_, int WM_, int WN_, int NBUF_>
+// A BM x BN tile by WM x WN waves with NBUF stages in LDS, 2 or 4 (a stage is loaded NBUF stages ahead). The scales of SG
+// groups of two stages, 16 SG bytes per row, are loaded at once: with one group every lane of the load takes a line of its
+// own, which keeps the address unit as long as four loads of codes; two groups where LDS has the room (NBUF 4).
+template <int BM_, int BN_, int WM_, int WN_, int NBUF_, int SG_>
 struct Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NBUF = NBUF_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NBUF = NBUF_, SG = SG_;
   static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
   static constexpr int TM = BM / 16 / WM, TN = BN / 16 / WN;  // 16-row tiles per wave
   static constexpr int ROWS = BM + BN;                        // rows of both operands, A's first
   static constexpr int CODES = ROWS * GM_ROW_BYTES;           // bytes per stage
-  static constexpr int SCALES = ROWS * 16;                    // bytes per two stages
-  static constexpr int RING = NBUF * CODES + NBUF / 2 * SCALES;
+  static constexpr int SCALES = ROWS * 16 * SG;               // bytes per SG groups
+  static constexpr int SBUF = SG == 2 ? 2 : NBUF / 2;         // buffers of them
+  static constexpr int RING = NBUF * CODES + SBUF * SCALES;
   static constexpr int STAGE = 16 * (TN * 32 + 16);           // per wave: 16 rows of 16-bit outputs on their way out
   static constexpr int LDS = RING + WAVES * STAGE;
   static constexpr int SLOTS = CODES / 16 / THREADS;          // 16-byte direct loads per thread and stage
-  static constexpr int SSLOTS = (ROWS + THREADS - 1) / THREADS;  // the same of the scales, per two stages
+  static constexpr int SSLOTS = (ROWS * SG + THREADS - 1) / THREADS;  // the same of the scales, per SG groups
   static constexpr int OPS = TM + TN;                         // operands of a chunk, B's first
   static constexpr int READ_ROWS = TM > 2 ? TM * 3 / 4 : 1;   // row tiles of a chunk during which the next one's are read
   // direct loads of a thread that may be on their way when a stage has to be there: those of the NBUF - 2 stages
-  // behind the next one (half of them bring scales too)
-  static constexpr int BEHIND = (NBUF - 2) * SLOTS + (NBUF / 2 - 1) * SSLOTS;
-  static_assert((NBUF == 2 || NBUF == 4) && BEHIND + SLOTS < 64 && BM % (8 * WAVES) == 0 && ROWS % 64 == 0, "");
+  // behind the next one (with SG 1 half of them bring scales too)
+  static constexpr int BEHIND = (NBUF - 2) * SLOTS + (SG == 2 ? 0 : (NBUF / 2 - 1) * SSLOTS);
+  static_assert((SG == 1 || (SG == 2 && NBUF == 4)) && (NBUF == 2 || NBUF == 4) && BEHIND + SLOTS < 64 && BM % (8 * WAVES) == 0 && ROWS * SG % THREADS == 0, "");
 };
 
-__device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+__device__ __forceinline__ int swizzle(int row) { return row & 7; }
 
 // Every LDS read of this wave is done, and every direct load but the last N, and so are every wave's of the workgroup.
 template <int N>
@@ -78,16 +83,19 @@ __device__ __forceinline__ void issue_codes(const Sources& src, uint8_t* buf, ui
   }
 }
 
-// The direct loads of two stages' scales (`from`: 16 times the group): 64 rows per instruction, dealt to the waves.
+// The direct loads of SG groups' scales (`from`: 16 times the first group): 64 / SG rows per instruction, dealt to the waves.
+// With two groups per row, their order is swapped in rows 8 .. 15 of 16, which keeps the reads of one group off each
+// other's banks.
 template <class G>
 __device__ __forceinline__ void issue_scales(const Sources& src, uint8_t* buf, uint32_t from, int wave, int lane) {
 #pragma unroll
   for (int i = 0; i < G::SSLOTS; ++i) {
-    const int first = (G::WAVES * i + wave) * 64 % G::ROWS;  // with few rows two waves bring the same ones
-    const int row = first + lane;
-    auto* to = (__attribute__((address_space(3))) void*)(buf + first * 16);
-    if (first < G::BM) __builtin_amdgcn_raw_ptr_buffer_load_lds(src.as, to, 16, (uint32_t)(row * src.ldsa) + from, 0, 0, 0);
-    else __builtin_amdgcn_raw_ptr_buffer_load_lds(src.bs, to, 16, (uint32_t)((row - G::BM) * src.ldsb) + from, 0, 0, 0);
+    const int first = (G::WAVES * i + wave) * (64 / G::SG);
+    const int row = first + lane / G::SG;
+    const uint32_t at = from + (G::SG == 2 ? ((lane ^ row >> 3) & 1) * 16 : 0);
+    auto* to = (__attribute__((address_space(3))) void*)(buf + first * 16 * G::SG);
+    if (first < G::BM) __builtin_amdgcn_raw_ptr_buffer_load_lds(src.as, to, 16, (uint32_t)(row * src.ldsa) + at, 0, 0, 0);
+    else __builtin_amdgcn_raw_ptr_buffer_load_lds(src.bs, to, 16, (uint32_t)((row - G::BM) * src.ldsb) + at, 0, 0, 0);
   }
 }
 
@@ -155,7 +163,10 @@ struct Wave {
 
   // Stage st of group st / 2 is in buffer st % NBUF: with `ring` = group % (NBUF / 2), buffer 2 ring + st % 2.
   __device__ __forceinline__ uint8_t* codes(int ring, int half) const { return lds + (2 * ring + half) * G::CODES; }
-  __device__ __forceinline__ uint8_t* scales(int ring) const { return lds + G::NBUF * G::CODES + ring * G::SCALES; }
+  // The scales of a group are in buffer group / SG % SBUF.
+  __device__ __forceinline__ uint8_t* scales(int group) const {
+    return lds + G::NBUF * G::CODES + (G::SBUF == 1 ? 0 : group / G::SG % G::SBUF) * G::SCALES;
+  }
   static __device__ __forceinline__ int ring_of(int group) { return G::NBUF == 2 ? 0 : group & (G::NBUF / 2 - 1); }
   __device__ __forceinline__ u32x4 read_codes(uint32_t at, int ring, int half, int chunk, int t) const {
     return *reinterpret_cast<const u32x4*>(codes(ring, half) + (chunk ? at ^ 64u : at) + t * 16 * GM_ROW_BYTES);
@@ -163,9 +174,10 @@ struct Wave {
   __device__ __forceinline__ u32x4 read_op(int ring, int half, int chunk, int i) const {
     return i < G::TN ? read_codes(frag_b, ring, half, chunk, i) : read_codes(frag_a, ring, half, chunk, i - G::TN);
   }
-  __device__ __forceinline__ u32x4 read_raw(int ring, int i) const {
-    const uint32_t at = i < G::TN ? scale_b + 256 * i : scale_a + 256 * (i - G::TN);
-    return *reinterpret_cast<const u32x4*>(scales(ring) + at);
+  __device__ __forceinline__ u32x4 read_raw(int group, int i) const {
+    const uint32_t half = G::SG == 2 ? (group & 1) * 16 : 0;
+    const uint32_t at = i < G::TN ? (scale_b ^ half) + 256 * G::SG * i : (scale_a ^ half) + 256 * G::SG * (i - G::TN);
+    return *reinterpret_cast<const u32x4*>(scales(group) + at);
   }
   __device__ __forceinline__ uint32_t pick(int i, int group) const {
     return pick_scales(raw[i], lane >> 4) & (group == last_group ? tail : ~0u);
@@ -192,7 +204,7 @@ struct Wave {
         op[NC][i] = read_op(ring_of(C == 3 ? next : group), NH, NC, i);
       } else {
         constexpr int i = B::s0 + X - B::loads - B::ops;
-        raw[i] = read_raw(ring_of(next), i);
+        raw[i] = read_raw(next, i);
       }
       between<C, I, X + 1, END>(group, next, codes_from);
     }
@@ -213,7 +225,9 @@ struct Wave {
         for (int i = P::s0; i < P::s1; ++i) sc[1][i] = pick(i, next);
       }
       between<C, I, B::all * J / G::TN, B::all*(J + 1) / G::TN>(group, next, codes_from);
-      if constexpr (C == 1 && I == G::TM - 1 && J == G::TN - 1) issue_scales<G>(src, scales(ring_of(group)), scales_from, wave, lane);
+      if constexpr (C == 1 && I == G::TM - 1 && J == G::TN - 1) {
+        if (G::SG == 1 || !(group & 1)) issue_scales<G>(src, scales(group + G::NBUF / 2), scales_from, wave, lane);
+      }
       __builtin_amdgcn_sched_barrier(0);
       chunk<C, J + 1 < G::TN ? I : I + 1, J + 1 < G::TN ? J + 1 : 0>(group, next, codes_from, scales_from);
     }
@@ -304,7 +318,8 @@ __global__ void __launch_bounds__(G::THREADS, G::LDS > 80 * 1024 ? G::WAVES / 4 
   const int arow = w.wave / G::WN * (BM / G::WM), brow = BM + w.wave % G::WN * (BN / G::WN);
   const uint32_t at = n * GM_ROW_BYTES + ((g ^ swizzle(n)) << 4);
   w.frag_a = arow * GM_ROW_BYTES + at, w.frag_b = brow * GM_ROW_BYTES + at;
-  w.scale_a = (arow + n) * 16, w.scale_b = (brow + n) * 16;
+  const uint32_t scale_at = G::SG * 16 * n + (G::SG == 2 ? (n >> 3) * 16 : 0);
+  w.scale_a = G::SG * 16 * arow + scale_at, w.scale_b = G::SG * 16 * brow + scale_at;
 
   // tile `id`: its place, and the sources of its loads
   const auto job_of = [&](int id) {
@@ -323,7 +338,7 @@ __global__ void __launch_bounds__(G::THREADS, G::LDS > 80 * 1024 ? G::WAVES / 4 
     w.src.bs = fp4::make_rsrc(static_cast<const uint8_t*>(b.s) + j.n0 * b.lds, (uint32_t)((mb - 1) * (int)b.lds + sbytes));
   };
   const auto codes_from = [](int st, int end) { return st < end ? (uint32_t)st * GM_ROW_BYTES : NOTHING; };
-  const auto scales_from = [](int st, int end) { return st < end ? (uint32_t)(st >> 1) * 16 : NOTHING; };
+  const auto scales_from = [](int st, int end) { return st < end ? (uint32_t)((st >> 1) / G::SG * G::SG) * 16 : NOTHING; };
 
   int id = blockIdx.x;
   Job job = job_of(id);
@@ -332,13 +347,14 @@ __global__ void __launch_bounds__(G::THREADS, G::LDS > 80 * 1024 ? G::WAVES / 4 
   for (int i = 0; i < NBUF; ++i) {
     const int st = job.s0 + i, ring = w.ring_of(st >> 1);
     issue_codes<G, 0, G::SLOTS>(w.src, w.codes(ring, i & 1), codes_from(st, job.s1), w.wave, w.lane);
-    if (!(i & 1)) issue_scales<G>(w.src, w.scales(ring), scales_from(st, job.s1), w.wave, w.lane);
+    if (!(i & 1) && (G::SG == 1 || i == 0 || !(st >> 1 & 1)))
+      issue_scales<G>(w.src, w.scales(st >> 1), scales_from(st, job.s1), w.wave, w.lane);
   }
   wait_and_meet<G::BEHIND + G::SLOTS>();
 #pragma unroll
   for (int i = 0; i < G::OPS; ++i) {
     w.op[0][i] = w.read_op(w.ring_of(job.s0 >> 1), 0, 0, i);
-    w.raw[i] = w.read_raw(w.ring_of(job.s0 >> 1), i);
+    w.raw[i] = w.read_raw(job.s0 >> 1, i);
   }
 #pragma unroll
   for (int i = 0; i < G::OPS; ++i) w.sc[0][i] = w.pick(i, job.s0 >> 1);
@@ -430,7 +446,7 @@ static double tiles_us(const TileCost& c, int64_t work, int stages, int cus) {
 
 // The cheapest of the tiles and K parts by those figures. Parts (only where one round of tiles leaves units idle) cost a
 // second kernel and their planes' way to memory and back: 2.5 us and 1.2 bytes per picosecond. For example 333 x 2560,
-// K = 9728: tiles of 64 take 13.9 us, of 128 29.9 us; 64 x 2560, K = 9728: 14.2 us, in 4 parts 9.8 us.
+// K = 9728: tiles of 64 take 13.1 us, of 128 28.9 us; 64 x 2560, K = 9728: 12.8 us, in 4 parts 9.3 us.
 // Where the last round of tiles of 256 would be a small one (split), the columns that fill whole rounds are one product and
 // the others a second in tiles that fill the device.
 static Plan plan_of(int64_t M, int64_t N, int64_t K, bool split = true) {
@@ -518,9 +534,9 @@ static int run_product(Plan p, int out_type, int64_t M, int64_t N, int64_t K, co
                        static_cast<uint8_t*>(y) + n * elem_bytes(out_type), ldy, nullptr, 0, st);
   }
   const auto launch = [&](auto fn) { return fn(p, out_type, (int)M, (int)N, (int)K, a, b, y, ldy, ws, st); };
-  if (p.tile == 256) return launch(launch_gemm<Tile<256, 256, 2, 2, 2>>);
-  if (p.tile == 128) return launch(launch_gemm<Tile<128, 128, 2, 2, 2>>);
-  return launch(launch_gemm<Tile<64, 64, 2, 2, 4>>);
+  if (p.tile == 256) return launch(launch_gemm<Tile<256, 256, 2, 2, 2, 1>>);
+  if (p.tile == 128) return launch(launch_gemm<Tile<128, 128, 2, 2, 2, 1>>);
+  return launch(launch_gemm<Tile<64, 64, 2, 2, 4, 2>>);
 }
 
 static int check_product(int out_type, int64_t M, int64_t N, int64_t K) {
