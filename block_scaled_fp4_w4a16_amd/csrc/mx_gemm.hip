@@ -456,10 +456,10 @@ static Plan plan_of(int64_t M, int64_t N, int64_t K, bool split = true) {
   p.parts = 1;
   p.per = (stages + 1) & ~1;
   p.us = 1e30;
-  // up to 16 rows: rows_kernel, by its chunk pairs and tiles of 16 (4096 x 4096 at M = 1 and 16: 3.6 and 4.6 us, tiles of 64
-  // 7.2; 14336 x 4096: 9.2 and 12.9 us against 7.8 and 8.1)
-  if (M <= 16) p.us = 1.8 + (double)((N + 15) / 16) * stages * (0.00046 + 0.000022 * M);
-  const double least = 2.5 + N * K * (17 / 32.) / 5e6;  // the weights' bytes at 5 TB/s
+  // up to 16 rows: rows_kernel, by its chunk pairs and tiles of 16 (4096 x 4096 at M = 1 and 16: 2.8 and 3.2 us, tiles of 64
+  // 7.2; 28672 x 8192: 26.4 and 31.9 us against 25.9 and 27.0)
+  if (M <= 16) p.us = 1.8 + (double)((N + 15) / 16) * stages * (0.00034 + 0.00001 * M);
+  const double least = 3.5 + N * K * (17 / 32.) / 5e6;  // the weights' bytes at 5 TB/s
   for (const TileCost& c : TILE_COSTS) {
     const int64_t tiles = ((M + c.tile - 1) / c.tile) * ((N + c.tile - 1) / c.tile);
     for (int want = 1; want <= 16; want *= 2) {
@@ -555,10 +555,11 @@ static int check_output(int out_type, int64_t N, const void* y, int64_t ldy) {
 }
 
 // Whether dense activations are quantised inside the product, else into the workspace before it. Each workgroup of 16
-// weight rows then quantises all of them again, which pays while its rounds are few: 4096 x 4096 at M = 1 and 9 takes 4.5
-// and 5.8 us against 5.5 and 6.2 in two kernels, 9728 x 2560 6.8 against 6.7, 14336 x 4096 at M = 16 27 against 11.
+// weight rows then quantises all of them again, which pays while rows and rounds are few: 4096 x 4096 at M = 1, 4 and 8 takes
+// 4.2, 4.6 and 5.3 us against 4.8, 4.9 and 5.1 in two kernels, 9728 x 2560 at M = 1 and 4 5.9 and 6.7 against 6.4 and 6.8,
+// 14336 x 4096 at M = 1 12.3 against 9.5.
 static bool fused(int64_t M, int64_t N, int64_t K) {
-  return M <= 16 && (N + 15) / 16 * ((blocks_of(K) + 7) / 8) <= 5120;
+  return M <= 16 && (N + 15) / 16 * ((blocks_of(K) + 7) / 8) * (M + 3) <= 32768;
 }
 
 struct LinearSpace {
