@@ -14,6 +14,8 @@
  *
  * with e2m1 in {0, +-0.5, +-1, +-1.5, +-2, +-3, +-4, +-6}, codebook10 in {0, +-1, +-2,
  * +-3, +-4, +-6, +-8, +-10}, g the per-matrix FP32 global scale (1.0 for ROCmFP4 and Q4_0).
+ * The MXFP4 entry points at the end of this file (fp4_quantize_mxfp4, fp4_dequant_mxfp4, w4a4_matmul,
+ * w4a4_linear) are products with both operands in 4 bits; their operation, shapes and alignments are stated there.
  * The library computes level*scale exactly, applies g last (fl32(fl32(level*scale)*g)),
  * and accumulates in FP32.
  *
@@ -38,7 +40,7 @@
  *    the static device array of w4a16_gemm_noalloc (FP4_GEMM_SCRATCH_BYTES per GPU), which
  *    only that entry point touches. Apart from those two, concurrent calls on different
  *    streams share no mutable state.
- *  - Shapes: W is N x K (N outputs, K inputs); x is M x K bf16 row-major; y is M x N
+ *  - Shapes (but of the MXFP4 entry points): W is N x K (N outputs, K inputs); x is M x K bf16 row-major; y is M x N
  *    fp32 row-major. K must be a multiple of 16 (NVFP4) or 32 (ROCmFP4). M = 0 is a
  *    no-op. x and the planes must be 16-byte aligned; y must be 4-byte aligned and must
  *    not overlap x or the planes.

@@ -6,6 +6,8 @@ the GPU library computes, written from the pages' definitions:
 * formats  - the E2M1, Codebook10, Q4_0, E4M3, UE4M3 and FP16 codes, RNE encoders;
 * layouts  - the canonical byte layouts of NVFP4, ROCmFP4 Dual / FAST and Q4_0;
 * ref      - exact dequantisation, the FP64 product y = x W^T and its bound;
+* mx       - MXFP4 quantisation, dequantisation and the product of two MXFP4
+             operands with its bound;
 * pack     - the data-free NVFP4 round-to-nearest packer, the ROCmFP4
              exhaustive finite-UE4M3 MSE scale search (C inner loop in csrc/)
              and the Q4_0 signed abs-max packer.
