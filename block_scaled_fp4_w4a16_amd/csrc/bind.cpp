@@ -189,11 +189,10 @@ void dequant(int64_t M, int64_t K, const Tensor& q, const Tensor& s, const Tenso
   check(fp4_dequant_mxfp4(type, M, K, &a, out.data_ptr(), ldo, current(d)), "fp4_dequant_mxfp4");
 }
 
-void matmul_into(int64_t M, int64_t N, int64_t K, const Operand& A, const Operand& B, const Tensor& y,
-                 const OptTensor& ws, c10::Device d) {
+void product_into(int64_t M, int64_t N, int64_t K, const fp4_mx& a, const fp4_mx& b, const Tensor& y, const OptTensor& ws,
+                  c10::Device d) {
   const int type = dense_type(y, "y");
   const int64_t ldy = rows_of(y, M, N, "y");
-  const fp4_mx a = operand(A.codes, A.scales, M, K, "A"), b = operand(B.codes, B.scales, N, K, "B");
   c10::DeviceGuard guard(d);
   const int64_t need = ws ? 0 : w4a4_matmul_workspace_bytes(M, N, K);
   check(need, "w4a4_matmul");
@@ -205,7 +204,7 @@ void matmul(int64_t M, int64_t N, int64_t K, const Tensor& aq, const Tensor& as,
             const Tensor& y, const py::object& stream, const OptTensor& ws) {
   const c10::Device d = one_device({&aq, &as, &bq, &bs, &y});
   const OnStream on(stream, d);
-  matmul_into(M, N, K, {aq, as}, {bq, bs}, y, ws, d);
+  product_into(M, N, K, operand(aq, as, M, K, "A"), operand(bq, bs, N, K, "B"), y, ws, d);
 }
 
 void linear_into(int64_t M, int64_t N, int64_t K, const Tensor& x, const Operand& B, const Tensor& y,
@@ -286,6 +285,36 @@ py::tuple from_canonical(const Tensor& codes, const Tensor& scales, std::optiona
 // y = Q(x) Q(w)^T. Rounding to MXFP4 counts as the identity in the backward pass, whose products are MXFP4 too:
 // dx = Q(g) Q(w^T)^T contracts N, dw = Q(g^T) Q(x^T)^T contracts the rows of x, each operand quantised along the axis
 // contracted. The transposed operands are made with the forward ones, from one reading of x and of w.
+// An operand in one allocation (each costs over a microsecond): its codes, then its scales.
+struct Held {
+  Tensor memory;
+  fp4_mx a{};
+};
+
+fp4_mx in_memory(const Tensor& memory, int64_t rows, int64_t k) {
+  const int64_t nb = blocks_of(k);
+  auto* p = static_cast<uint8_t*>(memory.data_ptr());
+  return {p, p + rows * 16 * nb, 16 * nb, (nb + 3) / 4 * 4};
+}
+
+Held new_held(int64_t rows, int64_t k, c10::Device d) {
+  const int64_t nb = blocks_of(k);
+  Held h;
+  h.memory = at::empty({rows * (16 * nb + (nb + 3) / 4 * 4)}, at::TensorOptions().dtype(at::kByte).device(d));
+  h.a = in_memory(h.memory, rows, k);
+  return h;
+}
+
+// m along its rows and, if asked, along its columns.
+void quantize_held(const Tensor& m, Held* rows, Held* cols, c10::Device d) {
+  if (rows) *rows = new_held(m.size(0), m.size(1), d);
+  if (cols) *cols = new_held(m.size(1), m.size(0), d);
+  c10::DeviceGuard guard(d);
+  check(fp4_quantize_mxfp4(dense_type(m, "x"), m.size(0), m.size(1), m.data_ptr(), rows_of(m, m.size(0), m.size(1), "x"),
+                           rows ? &rows->a : nullptr, cols ? &cols->a : nullptr, current(d)),
+        "fp4_quantize_mxfp4");
+}
+
 struct MxLinear : torch::autograd::Function<MxLinear> {
   static Tensor forward(torch::autograd::AutogradContext* ctx, const Tensor& x, const Tensor& w, bool need_dx, bool need_dw) {
     const c10::Device d = x.device();
@@ -294,13 +323,14 @@ struct MxLinear : torch::autograd::Function<MxLinear> {
     std::vector<int64_t> shape = x.sizes().vec();
     shape.back() = n;
     Tensor y = at::empty(shape, x.options().requires_grad(false).memory_format(at::MemoryFormat::Contiguous));
-    Operand xt, wt;
+    Held xt, wt;
     if (m > 0) {
-      Quantized wq = quantize_new(wm, true, need_dx, d), xq = quantize_new(xm, true, need_dw, d);
-      matmul_into(m, n, k, xq.first, wq.first, y.view({m, n}), {}, d);
-      wt = std::move(wq.second), xt = std::move(xq.second);
+      Held wq, xq;
+      quantize_held(wm, &wq, need_dx ? &wt : nullptr, d);
+      quantize_held(xm, &xq, need_dw ? &xt : nullptr, d);
+      product_into(m, n, k, xq.a, wq.a, y.view({m, n}), {}, d);
     }
-    ctx->save_for_backward({xt.codes, xt.scales, wt.codes, wt.scales});
+    ctx->save_for_backward({xt.memory, wt.memory});
     ctx->saved_data["shape"] = x.sizes().vec();
     ctx->saved_data["types"] = std::vector<int64_t>{(int64_t)x.scalar_type(), (int64_t)w.scalar_type()};
     return y;
@@ -320,10 +350,11 @@ struct MxLinear : torch::autograd::Function<MxLinear> {
     if (m == 0) {
       if (need_dw) dw.zero_();
     } else if (need_dx || need_dw) {
-      const Quantized q = quantize_new(g, need_dx, need_dw, d);
+      Held rows, cols;
+      quantize_held(g, need_dx ? &rows : nullptr, need_dw ? &cols : nullptr, d);
       const auto saved = ctx->get_saved_variables();
-      if (need_dx) matmul_into(m, k, n, q.first, {saved[2], saved[3]}, dx.view({m, k}), {}, d);
-      if (need_dw) matmul_into(n, k, m, q.second, {saved[0], saved[1]}, dw, {}, d);
+      if (need_dx) product_into(m, k, n, rows.a, in_memory(saved[1], k, n), dx.view({m, k}), {}, d);
+      if (need_dw) product_into(n, k, m, cols.a, in_memory(saved[0], k, m), dw, {}, d);
     }
     torch::autograd::variable_list out{dx, dw, Tensor(), Tensor()};
     if (at::GradMode::is_enabled()) {  // create_graph: the gradients have no derivative, and asking for one is an error
