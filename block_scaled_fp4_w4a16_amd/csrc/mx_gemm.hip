@@ -13,6 +13,11 @@
 // that chunk's start and the matrix core works through the reads and loads behind it.
 // Blocks past K: their scale bytes are replaced by 0 on both sides, which makes every product at most
 // 36 2^-254 = 0 in FP32, whatever the codes are. Rows past M or N load nothing and are not stored.
+// Tiles of 256 (64 KB of codes a stage, one workgroup per compute unit) are bound by power: 8192 x 14336 x 4096 takes 243 us,
+// 3.95 PFLOP/s; the same matrix instructions on random operands in registers alone reach 6.5 to 7.2 at 1.6 to 1.7 GHz.
+// Smaller tiles are for fewer outputs and are bound by their loads: 16 KB a stage of 64 x 64 outputs take 0.26 us on a
+// compute unit (64 bytes per ns), 0.41 for two workgroups at once; 333 x 2560 x 9728 13.0 us, 64 x 14336 x 4096 8.1 us
+// (33 MB, 4.1 TB/s).
 #include "mx.h"
 
 namespace mx {
@@ -210,9 +215,10 @@ struct Wave {
     }
   }
 
-  // Chunk C of `group` (`next` is the group after it) from its MFMA (I, J) on, a share of the other work behind each. A stage's second chunk ends the
-  // stage behind its first MFMA (every LDS read of the stage was issued in the chunk before) and issues the loads of the
-  // stage NBUF behind it (from byte `codes_from` of the codes and `scales_from` of the scales), whose buffer is free.
+  // Chunk C of `group` (`next` is the group after it) from its MFMA (I, J) on, a share of the other work behind each.
+  // A stage's second chunk ends the stage behind its first MFMA (every LDS read of the stage was issued in the chunk
+  // before) and issues the loads of the stage NBUF behind it (from byte `codes_from` of the codes and `scales_from` of
+  // the scales), whose buffer is free.
   template <int C, int I, int J>
   __device__ __forceinline__ void chunk(int group, int next, uint32_t codes_from, uint32_t scales_from) {
     if constexpr (I < G::TM) {
@@ -225,7 +231,7 @@ struct Wave {
         for (int i = P::s0; i < P::s1; ++i) sc[1][i] = pick(i, next);
       }
       between<C, I, B::all * J / G::TN, B::all*(J + 1) / G::TN>(group, next, codes_from);
-      if constexpr (C == 1 && I == G::TM - 1 && J == G::TN - 1) {
+      if constexpr (C == 1 && I == G::TM - 1 && J == G::TN - 1) {  // two groups' scales with the even one
         if (G::SG == 1 || !(group & 1)) issue_scales<G>(src, scales(group + G::NBUF / 2), scales_from, wave, lane);
       }
       __builtin_amdgcn_sched_barrier(0);

