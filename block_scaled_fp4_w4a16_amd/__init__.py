@@ -410,7 +410,8 @@ class PackedWeight:
 def fp4_quantize_mxfp4(M, K, x, q=None, s=None, qt=None, st=None, stream=None):
     """x [M, K] (float32, bfloat16 or float16; rows may be strided) -> MXFP4 along its rows into q [M, 16 ceil(K/32)] and
     s [M, ceil(K/32)], and / or along its columns into qt [K, 16 ceil(M/32)] and st [K, ceil(M/32)] (the transposed
-    operand). One of the two pairs may be None. Rows of the scales lie a multiple of 4 bytes apart."""
+    operand). One of the two pairs may be None. Rows of the scales lie a multiple of 4 bytes apart, and the bytes of s and
+    of st between a row's last scale and the next multiple of 4 are written as zeros."""
     _native.quantize(M, K, x, q, s, qt, st, stream)
 
 

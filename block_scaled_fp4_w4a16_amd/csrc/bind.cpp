@@ -53,9 +53,9 @@ fp4_mx operand(const Tensor& q, const Tensor& s, int64_t rows, int64_t k, const 
   const int64_t ldq = rows_of(q, rows, 16 * nb, what);
   int64_t lds = rows_of(s, rows, nb, what);
   if (rows == 1) lds = padded;
-  // rows of scales are read in whole dwords
+  // rows of scales are read and, by the quantisation, written in whole dwords
   if (rows > 0 && s.storage_offset() + (rows - 1) * lds + padded > (int64_t)s.storage().nbytes())
-    value_error(what, ": the last row of scales must be readable up to a multiple of 4 bytes");
+    value_error(what, ": the last row of scales must own its memory up to a multiple of 4 bytes");
   return {q.data_ptr(), s.data_ptr(), ldq, lds};
 }
 

@@ -315,7 +315,8 @@ int fp4_quantize_q4_0(int64_t N, int64_t K, const float* w, void* blocks, void* 
  * bytes at s + r * lds. That is the layout in which MXFP4 checkpoints hold their weights, so they need no
  * repacking. ldq and q are multiples of 16, lds and s of 4. When K is not a multiple of 32 the last block's
  * codes past K are zeros (in both operands; fp4_quantize_mxfp4 writes them so). Scale bytes of a row past its
- * last block, up to the next multiple of 4, are readable and ignored. ldq, lds and K are at most 2^22, rows at
+ * last block, up to the next multiple of 4, belong to the operand: fp4_quantize_mxfp4 writes zeros there, the other
+ * calls may read them and ignore what they hold. ldq, lds and K are at most 2^22, rows at
  * most 2^30; what would take a launch of 2^32 work items or more (past 10^8 weight rows in a product of few rows,
  * 2^36 outputs in small tiles) is refused with FP4_ERR_UNSUPPORTED.
  *
@@ -344,7 +345,7 @@ typedef struct fp4_mx {
  * Per block, with a the largest magnitude: s = max(floor(log2 a) - 2 + 127, 0), each value divided by
  * 2^(s - 127) and rounded to the nearest E2M1 value, halves to the even code, at most 6 in magnitude. A block
  * that holds an infinity or a NaN gets s = 255 and zero codes. The sign of a value that rounds to zero is kept.
- * Scale bytes of `rows` past a row's last block, up to the next multiple of 4, are written as zeros.
+ * Scale bytes of `rows` and of `cols` past a row's last block, up to the next multiple of 4, are written as zeros.
  * M = 0 is a no-op. Errors: FP4_ERR_ARG (unknown type; null x, q or s; neither rows nor cols), FP4_ERR_SHAPE
  * (M, K or a stride too small), FP4_ERR_UNSUPPORTED (K, a stride or, with cols, M too large), FP4_ERR_ALIGN, FP4_ERR_HIP.
  */
