@@ -4,8 +4,8 @@ Argument marshalling only: every function below checks tensor devices, dtypes an
 passes raw device pointers and the current HIP stream to the C entry point of the same
 name in libfp4w4a16.so, and raises RuntimeError on a negative status (the MXFP4 operators
 do so in _fp4bind.so, the binding's native half). All computation runs in the library's HIP
-kernels; there is no fallback path. Importing this package without the built libraries fails
-loudly.
+kernels; there is no fallback path. Importing this package without the C library fails loudly;
+without the native half, the MXFP4 calls do.
 """
 from __future__ import annotations
 
@@ -92,7 +92,24 @@ def lib() -> ctypes.CDLL:
 
 lib()  # fail at import time when the HIP library is absent
 
-from . import _fp4bind as _native  # noqa: E402  (links libfp4w4a16.so, loaded above)
+class _MissingNative:
+    """Stands for _fp4bind.so where it cannot be loaded: the W4A16 calls need only the C library and work without it,
+    each MXFP4 call raises."""
+
+    def __init__(self, cause: ImportError):
+        self._cause = cause
+
+    def __getattr__(self, name):
+        if name.startswith("__"):
+            raise AttributeError(name)
+        raise ImportError("the MXFP4 operators need _fp4bind.so, built for the installed torch: build it with "
+                          f"block_scaled_fp4_w4a16_amd/build.py (or __graft_entry__.build()); {self._cause}") from self._cause
+
+
+try:
+    from . import _fp4bind as _native  # noqa: E402  (links libfp4w4a16.so, loaded above)
+except ImportError as _cause:  # not built, or built for another torch
+    _native = _MissingNative(_cause)
 
 
 def _fmt(fmt) -> int:
