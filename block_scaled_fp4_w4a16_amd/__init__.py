@@ -406,6 +406,7 @@ class PackedWeight:
         return PackedWeight.from_canonical(fmt, N, K, blocks, None, 1.0, stream=stream)
 
     def matmul(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """x W^T [M, N]; outside autograd: the result has no gradient, whether or not x requires one."""
         M = x.shape[0]
         if x.shape[-1] != self.K:
             raise ValueError("x's last dimension must be K")
@@ -461,7 +462,8 @@ def w4a4_matmul(M, N, K, aq, a_s, bq, bs, y, stream=None, workspace=None):
 
 
 def w4a4_linear(M, N, K, x, bq, bs, y, stream=None, workspace=None):
-    """y [M, N] = Q(x) B^T: dense x [M, K] quantised along its rows, times an MXFP4 operand of depth K."""
+    """y [M, N] = Q(x) B^T: dense x [M, K] quantised along its rows, times an MXFP4 operand of depth K. No
+    gradient is computed: x or y that requires one is refused while gradients are enabled."""
     _native.linear(M, N, K, x, bq, bs, y, stream, workspace)
 
 
@@ -514,7 +516,8 @@ class MXTensor:
 
     def matmul(self, x, out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
                stream=None, workspace: torch.Tensor | None = None) -> torch.Tensor:
-        """x self^T [M, rows], self the weights: x an MXTensor of the same K, or dense [M, K], quantised on the way."""
+        """x self^T [M, rows], self the weights: x an MXTensor of the same K, or dense [M, K], quantised on the way. No
+        gradient is computed: dense x (or `out`) that requires one is refused while gradients are enabled."""
         if isinstance(x, MXTensor):
             if x.K != self.K:
                 raise ValueError(f"depths differ: {x.K} and {self.K}")

@@ -47,6 +47,14 @@ int64_t rows_of(const Tensor& t, int64_t rows, int64_t cols, const char* what) {
   return rows > 1 ? t.stride(0) : std::max<int64_t>(cols, 1);
 }
 
+// These calls run outside autograd. Rounding to codes has no gradient, as any conversion to whole numbers, but a dense
+// factor of a product has one, which must not get lost unseen, and neither must that of a tensor written over.
+void no_gradient(const Tensor& t, const char* what) {
+  if (at::GradMode::is_enabled() && t.requires_grad())
+    throw std::runtime_error(c10::str(what, " requires a gradient, which this call does not compute: detach it, call under "
+                                      "torch.no_grad(), or use mx_linear"));
+}
+
 fp4_mx operand(const Tensor& q, const Tensor& s, int64_t rows, int64_t k, const char* what) {
   if (q.scalar_type() != at::kByte || s.scalar_type() != at::kByte) type_error(what, ": codes and scales must be uint8");
   const int64_t nb = blocks_of(k), padded = (nb + 3) / 4 * 4;
@@ -181,6 +189,7 @@ py::tuple quantize_py(const Tensor& x, bool rows, bool cols, const py::object& s
 
 void dequant(int64_t M, int64_t K, const Tensor& q, const Tensor& s, const Tensor& out, const py::object& stream) {
   const int type = dense_type(out, "out", false);
+  no_gradient(out, "the output");
   const int64_t ldo = rows_of(out, M, K, "out");
   const c10::Device d = one_device({&q, &s, &out});
   const fp4_mx a = operand(q, s, M, K, "operand");
@@ -202,6 +211,7 @@ void product_into(int64_t M, int64_t N, int64_t K, const fp4_mx& a, const fp4_mx
 
 void matmul(int64_t M, int64_t N, int64_t K, const Tensor& aq, const Tensor& as, const Tensor& bq, const Tensor& bs,
             const Tensor& y, const py::object& stream, const OptTensor& ws) {
+  no_gradient(y, "the output");
   const c10::Device d = one_device({&aq, &as, &bq, &bs, &y});
   const OnStream on(stream, d);
   product_into(M, N, K, operand(aq, as, M, K, "A"), operand(bq, bs, N, K, "B"), y, ws, d);
@@ -221,6 +231,8 @@ void linear_into(int64_t M, int64_t N, int64_t K, const Tensor& x, const Operand
 
 void linear(int64_t M, int64_t N, int64_t K, const Tensor& x, const Tensor& bq, const Tensor& bs, const Tensor& y,
             const py::object& stream, const OptTensor& ws) {
+  no_gradient(x, "x");
+  no_gradient(y, "the output");
   const c10::Device d = one_device({&x, &bq, &bs, &y});
   const OnStream on(stream, d);
   linear_into(M, N, K, x, {bq, bs}, y, ws, d);
@@ -241,6 +253,7 @@ Tensor dequant_new(const Tensor& codes, const Tensor& scales, int64_t rows, int6
 
 Tensor matmul_new(const Tensor& aq, const Tensor& as, int64_t M, const Tensor& bq, const Tensor& bs, int64_t N, int64_t K,
                   const OptTensor& out, at::ScalarType dtype, const py::object& stream, const OptTensor& ws) {
+  if (out) no_gradient(*out, "the output");
   const OnStream on(stream, one_device({&bq, &bs}));
   Tensor y = output_of(out, M, N, dtype, bq.device());
   matmul(M, N, K, aq, as, bq, bs, y, py::none(), ws);
@@ -249,6 +262,8 @@ Tensor matmul_new(const Tensor& aq, const Tensor& as, int64_t M, const Tensor& b
 
 Tensor linear_new(const Tensor& x, const Tensor& bq, const Tensor& bs, int64_t N, int64_t K, const OptTensor& out,
                   at::ScalarType dtype, const py::object& stream, const OptTensor& ws) {
+  no_gradient(x, "x");
+  if (out) no_gradient(*out, "the output");
   if (x.dim() != 2) value_error("x must be [M, K] with the weights' K");
   if (x.size(1) != K) value_error("depths differ: ", x.size(1), " and ", K);
   const OnStream on(stream, one_device({&x, &bq, &bs}));

@@ -159,3 +159,25 @@ def test_python_refusals():
 
 def test_mx_struct_mirrors_the_header():
     assert ctypes.sizeof(fp4.Mx) == 32
+
+
+def test_calls_without_a_gradient_refuse_tensors_that_require_one():
+    t = torch.zeros(4, 64, dtype=torch.uint8)
+    w = fp4.MXTensor(t[:, :32], t[:, :2], 4, 64)
+    x, y = torch.zeros(3, 64), torch.zeros(3, 4)
+    for leaf in (x.clone().requires_grad_(), x.clone().requires_grad_() * 2, x.T.clone().requires_grad_().T):
+        with pytest.raises(RuntimeError, match="gradient"):
+            w.matmul(leaf)
+        with pytest.raises(RuntimeError, match="gradient"):
+            fp4.w4a4_linear(3, 4, 64, leaf, w.codes, w.scales, y)
+        for quiet in (leaf.detach(), x):
+            with pytest.raises(ValueError, match="GPU"):                 # goes on to the next check
+                w.matmul(quiet)
+        with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
+            w.matmul(leaf)
+    out = y.clone().requires_grad_()
+    for call in (lambda: w.matmul(w, out=out), lambda: w.matmul(x, out=out), lambda: fp4.w4a4_linear(3, 4, 64, x, w.codes, w.scales, out),
+                 lambda: fp4.w4a4_matmul(3, 4, 64, w.codes, w.scales, w.codes, w.scales, out),
+                 lambda: fp4.fp4_dequant_mxfp4(3, 4, w.codes, w.scales, out)):
+        with pytest.raises(RuntimeError, match="gradient"):
+            call()
