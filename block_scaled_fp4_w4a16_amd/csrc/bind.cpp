@@ -55,6 +55,11 @@ void no_gradient(const Tensor& t, const char* what) {
                                       "torch.no_grad(), or use mx_linear"));
 }
 
+// A kernel is about to write t's memory, which autograd does not see: a graph that saved t has to notice.
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 fp4_mx operand(const Tensor& q, const Tensor& s, int64_t rows, int64_t k, const char* what) {
   if (q.scalar_type() != at::kByte || s.scalar_type() != at::kByte) type_error(what, ": codes and scales must be uint8");
   const int64_t nb = blocks_of(k), padded = (nb + 3) / 4 * 4;
@@ -111,6 +116,7 @@ Workspace workspace_of(const OptTensor& given, int64_t need, c10::Device d) {
     if (given->device() != d) value_error("the workspace must live on the tensors' GPU");
     if (!given->is_contiguous()) value_error("tensors must be contiguous");
     w.hold = *given;
+    written(w.hold);
   } else if (need > 0) {
     w.hold = at::empty({need}, at::TensorOptions().dtype(at::kByte).device(d));
   } else {
@@ -142,6 +148,8 @@ void quantize(int64_t M, int64_t K, const Tensor& x, const OptTensor& q, const O
   rows_of(x, M, K, "x");
   const c10::Device d = one_device({&x, q ? &*q : &x, s ? &*s : &x, qt ? &*qt : &x, st_ ? &*st_ : &x});
   const OnStream on(stream, d);
+  for (const OptTensor* t : {&q, &s, &qt, &st_})
+    if (*t) written(**t);
   quantize_into(M, K, x, q ? &*q : nullptr, s ? &*s : nullptr, qt ? &*qt : nullptr, st_ ? &*st_ : nullptr, d);
 }
 
@@ -195,6 +203,7 @@ void dequant(int64_t M, int64_t K, const Tensor& q, const Tensor& s, const Tenso
   const fp4_mx a = operand(q, s, M, K, "operand");
   const OnStream on(stream, d);
   c10::DeviceGuard guard(d);
+  written(out);
   check(fp4_dequant_mxfp4(type, M, K, &a, out.data_ptr(), ldo, current(d)), "fp4_dequant_mxfp4");
 }
 
@@ -214,6 +223,7 @@ void matmul(int64_t M, int64_t N, int64_t K, const Tensor& aq, const Tensor& as,
   no_gradient(y, "the output");
   const c10::Device d = one_device({&aq, &as, &bq, &bs, &y});
   const OnStream on(stream, d);
+  written(y);
   product_into(M, N, K, operand(aq, as, M, K, "A"), operand(bq, bs, N, K, "B"), y, ws, d);
 }
 
@@ -235,6 +245,7 @@ void linear(int64_t M, int64_t N, int64_t K, const Tensor& x, const Tensor& bq, 
   no_gradient(y, "the output");
   const c10::Device d = one_device({&x, &bq, &bs, &y});
   const OnStream on(stream, d);
+  written(y);
   linear_into(M, N, K, x, {bq, bs}, y, ws, d);
 }
 

@@ -28,3 +28,31 @@ def test_quantize_writes_zeros_behind_a_rows_last_scale(axes, m, k):
         end = (nb + 3) // 4 * 4
         assert not held[:, nb:end].any() if on else (held == 0xA5).all()
         assert (held[:, end:] == 0xA5).all()
+
+
+def test_written_tensors_count_as_changed():
+    """Autograd refuses to go back through a saved tensor that a call wrote over, as it does for torch's own writes."""
+    m, n, k = 20, 48, 64
+    x = dense(m, k, torch.bfloat16, 210).cuda()
+    b = fp4.MXTensor.quantize(dense(n, k, torch.bfloat16, 211).cuda())
+    a = fp4.MXTensor.quantize(x)
+    scale = torch.ones(n, device="cuda", requires_grad=True)
+    for write in (lambda y: b.matmul(x, out=y), lambda y: b.matmul(a, out=y),
+                  lambda y: fp4.w4a4_linear(m, n, k, x, b.codes, b.scales, y),
+                  lambda y: fp4.w4a4_matmul(m, n, k, a.codes, a.scales, b.codes, b.scales, y)):
+        y = torch.randn(m, n, device="cuda")
+        loss = (y * scale).sum()
+        write(y)
+        with pytest.raises(RuntimeError, match="inplace"):
+            loss.backward()
+    out = torch.empty(m, k, device="cuda")
+    q, s, qt, st = (torch.zeros(*shape, dtype=torch.uint8, device="cuda") for shape in ((m, 32), (m, 4), (k, 16), (k, 4)))
+    before = [t._version for t in (out, q, s, qt, st)]
+    fp4.fp4_dequant_mxfp4(m, k, a.codes, a.scales, out)
+    fp4.fp4_quantize_mxfp4(m, k, x, q, s[:, :2], qt, st[:, :1])
+    assert all(t._version > v for t, v in zip((out, q, s, qt, st), before))
+    # the inputs are not written
+    assert x._version == a.codes._version == b.scales._version == 0
+    with torch.inference_mode():
+        y = torch.empty(m, n, device="cuda")
+    assert torch.equal(b.matmul(x, out=y), b.matmul(x))        # no version to count
