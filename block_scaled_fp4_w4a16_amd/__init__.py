@@ -422,7 +422,8 @@ class PackedWeight:
 
 
 # ----------------------------------------------------------------------------------------------
-# MXFP4 on both sides (W4A4): quantisation, products, a trainable linear layer
+# MXFP4 on both sides (W4A4): quantisation, products, a trainable linear layer. torch.jit.trace and make_fx would record
+# the allocations without the kernels: every call refuses to be traced.
 # ----------------------------------------------------------------------------------------------
 
 def fp4_quantize_mxfp4(M, K, x, q=None, s=None, qt=None, st=None, stream=None):

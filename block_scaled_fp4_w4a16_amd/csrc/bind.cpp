@@ -3,9 +3,11 @@
 // the same checks written in Python took 23 to 30 microseconds a call.
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/jit/frontend/tracer.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include "fp4w4a16.h"
@@ -23,6 +25,14 @@ template <typename... A>
 template <typename... A>
 [[noreturn]] void value_error(const A&... a) {
   throw py::value_error(c10::str(a...));
+}
+
+// A trace records what goes through torch's dispatcher, of these calls only the allocations: replayed, it would return
+// memory that nothing has written.
+void refuse_tracing() {
+  if (torch::jit::tracer::isTracing() ||
+      c10::impl::TorchDispatchModeTLS::get_mode(c10::impl::TorchDispatchModeKey::PROXY).has_value())
+    throw std::runtime_error("MXFP4 calls cannot be traced (torch.jit.trace, make_fx): their kernels would be missing from the graph");
 }
 
 int64_t blocks_of(int64_t k) { return (k + 31) / 32; }
@@ -143,6 +153,7 @@ void quantize_into(int64_t M, int64_t K, const Tensor& x, const Tensor* q, const
 
 void quantize(int64_t M, int64_t K, const Tensor& x, const OptTensor& q, const OptTensor& s, const OptTensor& qt,
               const OptTensor& st_, const py::object& stream) {
+  refuse_tracing();
   dense_type(x, "x");
   if (q.has_value() != s.has_value() || qt.has_value() != st_.has_value()) value_error("codes and scales come in pairs");
   rows_of(x, M, K, "x");
@@ -187,6 +198,7 @@ Quantized quantize_new(const Tensor& m, bool rows, bool cols, c10::Device d) {
 
 // (rows, K, codes, scales, codes along the columns, their scales)
 py::tuple quantize_py(const Tensor& x, bool rows, bool cols, const py::object& stream) {
+  refuse_tracing();
   dense_type(x, "x");
   const c10::Device d = one_device({&x});
   const OnStream on(stream, d);
@@ -196,6 +208,7 @@ py::tuple quantize_py(const Tensor& x, bool rows, bool cols, const py::object& s
 }
 
 void dequant(int64_t M, int64_t K, const Tensor& q, const Tensor& s, const Tensor& out, const py::object& stream) {
+  refuse_tracing();
   const int type = dense_type(out, "out", false);
   no_gradient(out, "the output");
   const int64_t ldo = rows_of(out, M, K, "out");
@@ -220,6 +233,7 @@ void product_into(int64_t M, int64_t N, int64_t K, const fp4_mx& a, const fp4_mx
 
 void matmul(int64_t M, int64_t N, int64_t K, const Tensor& aq, const Tensor& as, const Tensor& bq, const Tensor& bs,
             const Tensor& y, const py::object& stream, const OptTensor& ws) {
+  refuse_tracing();
   no_gradient(y, "the output");
   const c10::Device d = one_device({&aq, &as, &bq, &bs, &y});
   const OnStream on(stream, d);
@@ -241,6 +255,7 @@ void linear_into(int64_t M, int64_t N, int64_t K, const Tensor& x, const Operand
 
 void linear(int64_t M, int64_t N, int64_t K, const Tensor& x, const Tensor& bq, const Tensor& bs, const Tensor& y,
             const py::object& stream, const OptTensor& ws) {
+  refuse_tracing();
   no_gradient(x, "x");
   no_gradient(y, "the output");
   const c10::Device d = one_device({&x, &bq, &bs, &y});
@@ -256,6 +271,7 @@ Tensor output_of(const OptTensor& out, int64_t rows, int64_t cols, at::ScalarTyp
 
 Tensor dequant_new(const Tensor& codes, const Tensor& scales, int64_t rows, int64_t K, at::ScalarType dtype,
                    const py::object& stream) {
+  refuse_tracing();
   const OnStream on(stream, one_device({&codes, &scales}));
   Tensor out = output_of({}, rows, K, dtype, codes.device());
   dequant(rows, K, codes, scales, out, py::none());
@@ -264,6 +280,7 @@ Tensor dequant_new(const Tensor& codes, const Tensor& scales, int64_t rows, int6
 
 Tensor matmul_new(const Tensor& aq, const Tensor& as, int64_t M, const Tensor& bq, const Tensor& bs, int64_t N, int64_t K,
                   const OptTensor& out, at::ScalarType dtype, const py::object& stream, const OptTensor& ws) {
+  refuse_tracing();
   if (out) no_gradient(*out, "the output");
   const OnStream on(stream, one_device({&bq, &bs}));
   Tensor y = output_of(out, M, N, dtype, bq.device());
@@ -273,6 +290,7 @@ Tensor matmul_new(const Tensor& aq, const Tensor& as, int64_t M, const Tensor& b
 
 Tensor linear_new(const Tensor& x, const Tensor& bq, const Tensor& bs, int64_t N, int64_t K, const OptTensor& out,
                   at::ScalarType dtype, const py::object& stream, const OptTensor& ws) {
+  refuse_tracing();
   no_gradient(x, "x");
   if (out) no_gradient(*out, "the output");
   if (x.dim() != 2) value_error("x must be [M, K] with the weights' K");
@@ -395,6 +413,7 @@ struct MxLinear : torch::autograd::Function<MxLinear> {
 };
 
 Tensor mx_linear(const Tensor& x, const Tensor& w) {
+  refuse_tracing();
   dense_type(x, "x");
   dense_type(w, "w");
   if (x.dim() < 1 || w.dim() != 2 || x.size(-1) != w.size(1))

@@ -2,6 +2,7 @@
 anything is launched)."""
 import ctypes
 import itertools
+import warnings
 
 import numpy as np
 import pytest
@@ -181,3 +182,34 @@ def test_calls_without_a_gradient_refuse_tensors_that_require_one():
                  lambda: fp4.fp4_dequant_mxfp4(3, 4, w.codes, w.scales, out)):
         with pytest.raises(RuntimeError, match="gradient"):
             call()
+
+
+def test_traces_are_refused():
+    """A traced graph would hold the allocations without the kernels."""
+    from torch.fx.experimental.proxy_tensor import make_fx
+    t = torch.zeros(4, 64, dtype=torch.uint8)
+    q, s = t[:, :32], t[:, :2]
+    w = fp4.MXTensor(q, s, 4, 64)
+    x, y = torch.zeros(4, 64), torch.zeros(4, 4)
+
+    def into(call):
+        def f(x):
+            call(x)
+            return x + 1
+        return f
+
+    calls = [lambda x: w.matmul(x), lambda x: w.matmul(w) + x[:, :4], lambda x: fp4.mx_linear(x, x),
+             lambda x: fp4.MXTensor.quantize(x).codes, lambda x: fp4.MXTensor.quantize_both(x)[1].scales, lambda x: w.dequant() + x,
+             into(lambda x: fp4.fp4_quantize_mxfp4(4, 64, x, q, s)),
+             into(lambda x: fp4.fp4_dequant_mxfp4(4, 64, w.codes, w.scales, x)),
+             into(lambda x: fp4.w4a4_linear(4, 4, 64, x, w.codes, w.scales, y)),
+             into(lambda x: fp4.w4a4_matmul(4, 4, 64, w.codes, w.scales, w.codes, w.scales, y))]
+    for call in calls:
+        with pytest.raises(RuntimeError, match="traced"), warnings.catch_warnings():
+            warnings.simplefilter("ignore")                              # torch.jit.trace is deprecated
+            torch.jit.trace(call, (x,), check_trace=False)
+        for mode in ("real", "fake"):
+            with pytest.raises(RuntimeError, match="traced"):
+                make_fx(call, tracing_mode=mode)(x)
+    with pytest.raises(ValueError, match="GPU"):                         # outside a trace
+        w.matmul(x)
