@@ -52,6 +52,7 @@ int dense_type(const Tensor& t, const char* what, bool half = true) {
 int64_t rows_of(const Tensor& t, int64_t rows, int64_t cols, const char* what) {
   if (t.dim() != 2 || t.size(0) != rows || t.size(1) != cols)
     value_error(what, " must have shape [", rows, ", ", cols, "], not ", t.sizes());
+  if (t.is_neg()) value_error(what, " is a lazily negated view, whose memory has the other sign: resolve_neg() it first");
   if (cols > 1 && t.stride(1) != 1) value_error(what, ": the elements of a row must be contiguous");
   if (rows > 1 && t.stride(0) < cols) value_error(what, ": rows overlap");
   return rows > 1 ? t.stride(0) : std::max<int64_t>(cols, 1);
@@ -177,9 +178,10 @@ Operand new_operand(int64_t rows, int64_t k, c10::Device d) {
   return o;
 }
 
-// x [..., K] as a matrix whose rows are contiguous (a copy only where the strides ask for one).
-Tensor as_rows(const Tensor& x) {
-  if (x.dim() < 1) value_error("a tensor with at least one axis expected");
+// x [..., K] as a matrix whose rows are contiguous (a copy only where the strides or a lazy negation ask for one).
+Tensor as_rows(const Tensor& given) {
+  if (given.dim() < 1) value_error("a tensor with at least one axis expected");
+  const Tensor x = given.is_neg() ? given.resolve_neg() : given;
   Tensor m = x.dim() == 2 ? x : x.size(-1) > 0 ? x.reshape({x.numel() / x.size(-1), x.size(-1)}) : x.reshape({-1, 0});
   const bool ok = (m.size(1) <= 1 || m.stride(1) == 1) && (m.size(0) <= 1 || m.stride(0) >= m.size(1));
   return ok ? m : m.contiguous();

@@ -56,3 +56,28 @@ def test_written_tensors_count_as_changed():
     with torch.inference_mode():
         y = torch.empty(m, n, device="cuda")
     assert torch.equal(b.matmul(x, out=y), b.matmul(x))        # no version to count
+
+
+def test_lazily_negated_views():
+    """The imaginary part of a conjugate is a view whose memory holds the other sign."""
+    z = torch.complex(dense(70, 96, torch.float32, 220), dense(70, 96, torch.float32, 221)).cuda()
+    for part in (z.conj().imag, z[:, :1].conj().imag, z[0].conj().imag, torch._neg_view(z.real.contiguous())):
+        assert part.is_neg()
+        plain = part.resolve_neg().contiguous()
+        got, want = fp4.MXTensor.quantize_both(part), fp4.MXTensor.quantize_both(plain)
+        for g, w in zip(got, want):
+            assert torch.equal(g.codes, w.codes) and torch.equal(g.scales, w.scales)
+        b = fp4.MXTensor.quantize(dense(40, part.shape[-1], torch.float32, 222).cuda())
+        if part.dim() == 2:
+            assert torch.equal(b.matmul(part), b.matmul(plain))
+        w = dense(40, part.shape[-1], torch.float32, 223).cuda()
+        assert torch.equal(fp4.mx_linear(part, w), fp4.mx_linear(plain, w))
+    x, w = dense(70, 96, torch.float32, 224).cuda().requires_grad_(), dense(96, 96, torch.float32, 225).cuda().requires_grad_()
+    g = torch._neg_view(z.real.contiguous())
+    for got, want in zip(torch.autograd.grad(fp4.mx_linear(x, w), (x, w), g), torch.autograd.grad(fp4.mx_linear(x, w), (x, w), g.resolve_neg())):
+        assert torch.equal(got, want)
+    q, s = torch.empty(70, 48, dtype=torch.uint8, device="cuda"), torch.empty(70, 4, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="negated"):
+        fp4.fp4_quantize_mxfp4(70, 96, g, q, s[:, :3])
+    with pytest.raises(ValueError, match="negated"):
+        fp4.fp4_dequant_mxfp4(70, 96, q, s[:, :3], g)
