@@ -472,9 +472,10 @@ def w4a4_linear(M, N, K, x, bq, bs, y, stream=None, workspace=None):
 class MXTensor:
     """An MXFP4 operand: `rows` rows of `K` values, blocks of 32 along K (the last one padded with zeros).
 
-    A `stream` given to a method (a torch stream or a raw handle; None: the current one) takes the place of the current
-    stream for the whole call, its copies and allocations included: inputs have to be ready on it, and a result made for
-    it is used elsewhere as any tensor made under `torch.cuda.stream(stream)`."""
+    A `stream` given to a method (a torch stream or a raw handle, of the tensors' GPU; None: the current one) takes the
+    place of the current stream for the whole call, its copies and allocations included: inputs have to be ready on it, and
+    to live until it has read them (`record_stream` where they may be freed earlier), and a result made for it is used
+    elsewhere as any tensor made under `torch.cuda.stream(stream)`."""
     codes: torch.Tensor      # uint8 [rows, 16 ceil(K / 32)], element 2j in the low half of byte j
     scales: torch.Tensor     # uint8 [rows, ceil(K / 32)], E8M0; rows a multiple of 4 bytes apart
     rows: int

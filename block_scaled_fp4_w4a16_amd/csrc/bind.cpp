@@ -103,8 +103,14 @@ struct OnStream {
   std::optional<c10::hip::HIPStream> before;
   OnStream(const py::handle& stream, c10::Device d) {
     if (stream.is_none()) return;
-    const py::object h =
-        py::hasattr(stream, "cuda_stream") ? py::object(stream.attr("cuda_stream")) : py::reinterpret_borrow<py::object>(stream);
+    py::object h = py::reinterpret_borrow<py::object>(stream);
+    if (py::hasattr(stream, "cuda_stream")) {
+      // a kernel runs on its stream's GPU, which may not reach the tensors' memory
+      const py::object on = py::getattr(py::getattr(stream, "device", py::none()), "index", py::none());
+      if (!on.is_none() && on.cast<int64_t>() != d.index())
+        value_error("the stream belongs to GPU ", on.cast<int64_t>(), ", the tensors live on ", d);
+      h = stream.attr("cuda_stream");
+    }
     const auto raw = reinterpret_cast<hipStream_t>(h.cast<uintptr_t>());
     before = c10::hip::getCurrentHIPStream(d.index());
     c10::hip::setCurrentHIPStream(c10::hip::getStreamFromExternal(raw, d.index()));

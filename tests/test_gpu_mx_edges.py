@@ -81,3 +81,30 @@ def test_lazily_negated_views():
         fp4.fp4_quantize_mxfp4(70, 96, g, q, s[:, :3])
     with pytest.raises(ValueError, match="negated"):
         fp4.fp4_dequant_mxfp4(70, 96, q, s[:, :3], g)
+
+
+def test_a_stream_of_another_gpu_is_refused():
+    x = dense(20, 64, torch.bfloat16, 230).cuda()
+    b = fp4.MXTensor.quantize(dense(40, 64, torch.bfloat16, 231).cuda())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    want = b.matmul(x)
+
+    class Elsewhere:                                           # as a torch stream of a second GPU looks
+        cuda_stream, device = side.cuda_stream, torch.device("cuda", x.device.index + 1)
+
+    y, out = torch.empty(20, 40, device="cuda"), torch.empty(20, 64, device="cuda")
+    for call in (lambda s: fp4.MXTensor.quantize_both(x, stream=s), lambda s: b.matmul(x, stream=s), lambda s: b.matmul(b, stream=s),
+                 lambda s: b.dequant(stream=s), lambda s: fp4.w4a4_linear(20, 40, 64, x, b.codes, b.scales, y, stream=s),
+                 lambda s: fp4.w4a4_matmul(20, 40, 64, b.codes[:20], b.scales[:20], b.codes, b.scales, y, stream=s),
+                 lambda s: fp4.fp4_dequant_mxfp4(20, 64, b.codes[:20], b.scales[:20], out, stream=s),
+                 lambda s: fp4.fp4_quantize_mxfp4(20, 64, x, b.codes[:20], b.scales[:20], stream=s)):
+        with pytest.raises(ValueError, match="stream belongs"):
+            call(Elsewhere())
+    class Bare:                                                # a handle and nothing else
+        cuda_stream = side.cuda_stream
+
+    for s in (side, side.cuda_stream, Bare(), torch.cuda.current_stream(), 0):
+        got = b.matmul(x, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
