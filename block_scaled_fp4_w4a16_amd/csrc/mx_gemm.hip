@@ -126,6 +126,23 @@ __device__ __forceinline__ void mfma_acc(f32x4& acc, const u32x4& a, uint32_t sa
 #undef MX_MFMA_
 }
 
+// Sum number I from the end.
+template <class G, int I>
+__device__ __forceinline__ f32x4& sum_from_end(f32x4 (&acc)[G::TM][G::TN]) {
+  constexpr int at = G::TM * G::TN - 1 - I;
+  return acc[at / G::TN][at % G::TN];
+}
+template <class G>
+__device__ __forceinline__ void wait_for_sums(f32x4 (&acc)[G::TM][G::TN]) {
+#define MX_SUM(I) "+a"(sum_from_end<G, I>(acc))
+  if constexpr (G::TM * G::TN == 4)
+    asm volatile("s_nop 15\n\ts_nop 1" : MX_SUM(0), MX_SUM(1), MX_SUM(2), MX_SUM(3));
+  else
+    asm volatile("s_nop 15\n\ts_nop 1"
+                 : MX_SUM(0), MX_SUM(1), MX_SUM(2), MX_SUM(3), MX_SUM(4), MX_SUM(5), MX_SUM(6), MX_SUM(7));
+#undef MX_SUM
+}
+
 // Four dwords of a row's scales (four chunks of four blocks) -> byte c is block g of chunk c.
 __device__ __forceinline__ uint32_t pick_scales(const u32x4& w, int g) {
   const uint32_t sel = (uint32_t)g | (uint32_t)(4 + g) << 8;
@@ -376,7 +393,8 @@ __global__ void __launch_bounds__(G::THREADS, G::LDS > 80 * 1024 ? G::WAVES / 4 
     // Two stages (one group of scales) at a time; the stages NBUF ahead are loaded. Past the workgroup's last stage
     // nothing is: the look ahead reads what is in LDS and is not used. The second half of an odd count multiplies by
     // the zero scales of blocks past K. One loop body without branches serves every stage.
-    for (int st = job.s0; st < job.s1; st += 2) {
+    int st = job.s0;
+    do {  // a tile has a stage at least: the sums have one way out of the loop, with no copies of them before the wait
       int ahead = st + NBUF, end = job.s1, next_group = (st >> 1) + 1;
       if (st + 2 >= job.s1) {
         if (id < total) {  // only with NBUF = 2
@@ -393,11 +411,13 @@ __global__ void __launch_bounds__(G::THREADS, G::LDS > 80 * 1024 ? G::WAVES / 4 
 #pragma unroll
       for (int i = 0; i < G::OPS; ++i) w.sc[0][i] = w.sc[1][i];
       __builtin_amdgcn_sched_barrier(0);
-    }
+      st += 2;
+    } while (st < job.s1);
 
-    // the last MFMAs' results: 18 wait states before anything but an MFMA reads them, then every read of a sum is
-    // ordered behind the wait
-    asm volatile("s_nop 15\n\ts_nop 15");
+    // An MFMA's result needs eight wait states (4 passes) before anything but an MFMA reads it, and the compiler does not see
+    // these MFMAs. The last eight's sums go through the wait itself, so that no copy of them can come before it (a copy
+    // that the compiler made in front of a bare wait came after seven); every read of another sum is ordered behind it.
+    wait_for_sums<G>(w.acc);
 #pragma unroll
     for (int i = 0; i < G::TM; ++i)
 #pragma unroll
