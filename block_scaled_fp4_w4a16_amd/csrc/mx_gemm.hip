@@ -19,6 +19,7 @@
 // compute unit (64 bytes per ns), 0.41 for two workgroups at once; 333 x 2560 x 9728 13.0 us, 64 x 14336 x 4096 8.1 us
 // (33 MB, 4.1 TB/s).
 #include "mx.h"
+#include "mx_plan.h"
 
 namespace mx {
 
@@ -443,75 +444,6 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
   store4(out_type, y, row * ldy + col, sum, (int)(N - col), vec);
 }
 
-// How a product is run.
-struct Plan {
-  int tile;    // 0: rows_kernel, else gemm_kernel with tiles of 64, 128 or 256
-  int parts;   // K parts
-  int per;     // stages per part (even)
-  int64_t ldp; // floats per row of a plane
-  int64_t first_n;  // > 0: columns [0, first_n) in tiles of 256, the others as a product of their own
-  double us;   // what it is taken to cost
-};
-
-// What a tile costs, in microseconds as measured on 256 compute units: a launch with its first loads and last stores,
-// each further round's stores, and a stage of 256 positions with one workgroup on a unit (256: with every unit busy; a
-// few workgroups of 256 run a stage in 1.2) and with two (64 and 128: two fit; their stages run at 16 and 28 outputs per
-// nanosecond, those of 256 at 37).
-struct TileCost {
-  int tile;
-  double launch, round, one, two;
-};
-constexpr TileCost TILE_COSTS[] = {{64, 3.2, 0.6, 0.27, 0.5}, {128, 4.4, 1.6, 0.67, 1.15}, {256, 9.0, 4.0, 1.75, 0}};
-
-static double tiles_us(const TileCost& c, int64_t work, int stages, int cus) {
-  const int64_t slots = (c.two > 0 ? 2 : 1) * (int64_t)cus, full = work / slots, rest = work - full * slots;
-  double last = rest > cus ? c.two : c.one;
-  if (c.two == 0) last = 1.2 + (c.one - 1.2) * rest / cus;
-  return c.launch + (full + (rest > 0) - 1) * c.round + stages * (full * (c.two > 0 ? c.two : c.one) + (rest > 0 ? last : 0));
-}
-
-// The cheapest of the tiles and K parts by those figures. Parts (only where one round of tiles leaves units idle) cost a
-// second kernel and their planes' way to memory and back: 2.5 us and 1.2 bytes per picosecond. For example 333 x 2560,
-// K = 9728: tiles of 64 take 13.1 us, of 128 28.9 us; 64 x 2560, K = 9728: 12.8 us, in 4 parts 9.3 us.
-// Where the last round of tiles of 256 would be a small one (split), the columns that fill whole rounds are one product and
-// the others a second in tiles that fill the device.
-static Plan plan_of(int64_t M, int64_t N, int64_t K, bool split = true) {
-  Plan p{};
-  p.ldp = (N + 3) / 4 * 4;
-  const int stages = (int)((blocks_of(K) + 7) / 8), cus = fp4_device_cus();
-  p.parts = 1;
-  p.per = (stages + 1) & ~1;
-  p.us = 1e30;
-  // up to 16 rows: rows_kernel, by its chunk pairs and tiles of 16 (4096 x 4096 at M = 1 and 16: 2.8 and 3.2 us, tiles of 64
-  // 7.2; 28672 x 8192: 26.4 and 31.9 us against 25.9 and 27.0)
-  if (M <= 16) p.us = 1.8 + (double)((N + 15) / 16) * stages * (0.00034 + 0.00001 * M);
-  const double least = 3.5 + N * K * (17 / 32.) / 5e6;  // the weights' bytes at 5 TB/s
-  for (const TileCost& c : TILE_COSTS) {
-    const int64_t tiles = ((M + c.tile - 1) / c.tile) * ((N + c.tile - 1) / c.tile);
-    for (int want = 1; want <= 16; want *= 2) {
-      const int per = ((stages + want - 1) / want + 1) & ~1, parts = (stages + per - 1) / per;
-      if (want > 1 && (c.tile == 256 || parts != want || tiles * parts > cus)) break;
-      double us = tiles_us(c, tiles * parts, per, cus);
-      if (us < least) us = least;
-      if (parts > 1) us += 2.5 + parts * M * p.ldp * 4 / 1.2e6;
-      if (us < p.us) p.us = us, p.tile = c.tile, p.parts = parts, p.per = per;
-    }
-  }
-  if (split) {
-    const TileCost& c = TILE_COSTS[2];
-    const int64_t down = (M + 255) / 256, across = (N + 255) / 256, fit = down * across / cus * cus / down;
-    if (fit > 0 && fit < across) {
-      const Plan rest = plan_of(M, N - fit * 256, K, false);
-      const double us = tiles_us(c, down * fit, (stages + 1) & ~1, cus) + rest.us;
-      if (rest.parts == 1 && us < 0.95 * p.us)
-        p.us = us, p.tile = 256, p.parts = 1, p.per = (stages + 1) & ~1, p.first_n = fit * 256;
-    }
-  }
-  return p;
-}
-
-static int64_t plane_bytes(const Plan& p, int64_t M) { return p.parts > 1 ? p.parts * M * p.ldp * 4 : 0; }
-
 template <class G, int OUT>
 static int launch_tiles(const Plan& p, int M, int N, int K, const fp4_mx& a, const fp4_mx& b, void* y, int64_t ldy,
                         hipStream_t st) {
@@ -549,14 +481,14 @@ static int run_product(Plan p, int out_type, int64_t M, int64_t N, int64_t K, co
   if (p.tile == 0) return launch_rows(0, out_type, (int)M, (int)N, (int)K, nullptr, 0, &a, b, y, ldy, st);
   if (p.parts > 1 && (!ws || ws_bytes < (size_t)plane_bytes(p, M))) {
     p.parts = 1;
-    p.per = ((int)((blocks_of(K) + 7) / 8) + 1) & ~1;
+    p.per = (stages_of(K) + 1) & ~1;
   }
   if (p.first_n > 0) {
     const int64_t n = p.first_n;
     p.first_n = 0;
     if (int rc = run_product(p, out_type, M, n, K, a, b, y, ldy, nullptr, 0, st)) return rc;
     const fp4_mx rest = {static_cast<uint8_t*>(b.q) + n * b.ldq, static_cast<uint8_t*>(b.s) + n * b.lds, b.ldq, b.lds};
-    return run_product(plan_of(M, N - n, K, false), out_type, M, N - n, K, a, rest,
+    return run_product(plan_of(M, N - n, K, fp4_device_cus(), false), out_type, M, N - n, K, a, rest,
                        static_cast<uint8_t*>(y) + n * elem_bytes(out_type), ldy, nullptr, 0, st);
   }
   const auto launch = [&](auto fn) { return fn(p, out_type, (int)M, (int)N, (int)K, a, b, y, ldy, ws, st); };
@@ -580,14 +512,6 @@ static int check_output(int out_type, int64_t N, const void* y, int64_t ldy) {
   return fp4_aligned(y, (uintptr_t)elem_bytes(out_type)) ? FP4_OK : FP4_ERR_ALIGN;
 }
 
-// Whether dense activations are quantised inside the product, else into the workspace before it. Each workgroup of 16
-// weight rows then quantises all of them again, which pays while rows and rounds are few: 4096 x 4096 at M = 1, 4 and 8 takes
-// 4.2, 4.6 and 5.3 us against 4.8, 4.9 and 5.1 in two kernels, 9728 x 2560 at M = 1 and 4 5.9 and 6.7 against 6.4 and 6.8,
-// 14336 x 4096 at M = 1 12.3 against 9.5.
-static bool fused(int64_t M, int64_t N, int64_t K) {
-  return M <= 16 && (N + 15) / 16 * ((blocks_of(K) + 7) / 8) * (M + 3) <= 32768;
-}
-
 struct LinearSpace {
   int64_t q, s, planes;  // bytes, each a multiple of 256
 };
@@ -603,7 +527,7 @@ using namespace mx;
 
 extern "C" int64_t w4a4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (int rc = check_product(FP4_TYPE_F32, M, N, K)) return rc;
-  return M == 0 ? 0 : plane_bytes(plan_of(M, N, K), M);
+  return M == 0 ? 0 : plane_bytes(plan_of(M, N, K, fp4_device_cus()), M);
 }
 
 extern "C" int w4a4_matmul(int out_type, int64_t M, int64_t N, int64_t K, const fp4_mx* a, const fp4_mx* b, void* y,
@@ -614,14 +538,14 @@ extern "C" int w4a4_matmul(int out_type, int64_t M, int64_t N, int64_t K, const 
   if (int rc = check_operand(b, K)) return rc;
   if (int rc = check_output(out_type, N, y, ldy)) return rc;
   if (workspace && !fp4_aligned(workspace, 16)) return FP4_ERR_ALIGN;
-  return run_product(plan_of(M, N, K), out_type, M, N, K, *a, *b, y, ldy, workspace, workspace_bytes,
+  return run_product(plan_of(M, N, K, fp4_device_cus()), out_type, M, N, K, *a, *b, y, ldy, workspace, workspace_bytes,
                      static_cast<hipStream_t>(stream));
 }
 
 extern "C" int64_t w4a4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (int rc = check_product(FP4_TYPE_F32, M, N, K)) return rc;
   if (M == 0 || fused(M, N, K)) return 0;
-  const LinearSpace sp = linear_space(plan_of(M, N, K), M, K);
+  const LinearSpace sp = linear_space(plan_of(M, N, K, fp4_device_cus()), M, K);
   return sp.q + sp.s + sp.planes;
 }
 
@@ -639,7 +563,7 @@ extern "C" int w4a4_linear(int x_type, int out_type, int64_t M, int64_t N, int64
   if (workspace && !fp4_aligned(workspace, 16)) return FP4_ERR_ALIGN;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (fused(M, N, K)) return launch_rows(x_type, out_type, (int)M, (int)N, (int)K, x, ldx, nullptr, *b, y, ldy, st);
-  const Plan p = plan_of(M, N, K);
+  const Plan p = plan_of(M, N, K, fp4_device_cus());
   const LinearSpace sp = linear_space(p, M, K);
   if (!workspace || workspace_bytes < (size_t)(sp.q + sp.s)) return FP4_ERR_ARG;
   auto* w = static_cast<uint8_t*>(workspace);
