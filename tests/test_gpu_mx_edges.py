@@ -1,4 +1,7 @@
 """MXFP4 on the GPU: what the calls do to the memory, streams and gradients around them."""
+from concurrent.futures import ThreadPoolExecutor
+
+import numpy as np
 import pytest
 import torch
 
@@ -108,3 +111,52 @@ def test_a_stream_of_another_gpu_is_refused():
         got = b.matmul(x, stream=s)
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("m", [3, 40, 150])
+@pytest.mark.parametrize("e", [-120, -126, -130, -138, -147])
+def test_sums_below_the_normal_range(m, e):
+    """Scales whose product is 2^e: every product is a multiple of 2^(e - 2), at least FP32's smallest step, and the sum of
+    96 of them, at most 36 2^e each, has under 24 bits above it. So every sum, subnormal or not, is exact."""
+    n, k, sa = 130, 96, 60
+    r = np.random.default_rng([m, -e])
+    a = r.integers(0, 256, (m, 48), dtype=np.uint8), np.full((m, 3), sa, np.uint8)
+    b = r.integers(0, 256, (n, 48), dtype=np.uint8), np.full((n, 3), 254 + e - sa, np.uint8)
+    ta, tb = (fp4.MXTensor.from_canonical(torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda(), k) for q, s in (a, b))
+    ref, _ = mx.product(mx.dequant(*a), mx.dequant(*b))
+    assert (np.abs(ref) < 2.0 ** -126).any() or e == -120
+    assert np.array_equal(tb.matmul(ta).cpu().double().numpy(), ref)
+
+
+@pytest.mark.parametrize("what", ["dense", "MXFP4", "layer"])
+def test_two_threads_on_two_streams(what):
+    """Each thread's calls are counted and its errors are raised here."""
+    m, n, k, times = 40, 200, 8192, 20
+    w = dense(n, k, torch.bfloat16, 240).cuda()
+    b = fp4.MXTensor.quantize(w)
+    assert fp4.w4a4_matmul_workspace_bytes(m, n, k) > 0
+    xs = [dense(m, k, torch.bfloat16, 241 + i).cuda() for i in range(2)]
+
+    def call(x):
+        if what == "layer":
+            x, v = x.detach().requires_grad_(), w.detach().requires_grad_()
+            y = fp4.mx_linear(x, v)
+            return y.detach(), *torch.autograd.grad(y, (x, v), torch.ones_like(y))
+        return (b.matmul(x if what == "dense" else fp4.MXTensor.quantize(x)),)
+
+    want = [call(x) for x in xs]
+    torch.cuda.synchronize()
+    done = [0, 0]
+
+    def run(i):
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            for _ in range(times):
+                got = call(xs[i])
+                side.synchronize()
+                done[i] += all(torch.equal(g, v) for g, v in zip(got, want[i]))
+
+    with ThreadPoolExecutor(2) as pool:
+        for f in [pool.submit(run, i) for i in range(2)]:
+            f.result(timeout=60)
+    assert done == [times, times]
