@@ -160,3 +160,62 @@ def test_two_threads_on_two_streams(what):
         for f in [pool.submit(run, i) for i in range(2)]:
             f.result(timeout=60)
     assert done == [times, times]
+
+
+def test_layer_in_inference_mode():
+    x, w = dense(24, 64, torch.bfloat16, 250).cuda(), dense(40, 64, torch.float32, 251).cuda().requires_grad_()
+    want = fp4.mx_linear(x, w.detach())
+    with torch.inference_mode():
+        y = fp4.mx_linear(x.clone(), w)
+        assert y.is_inference() and torch.equal(y, want)
+        b = fp4.MXTensor.quantize(w)
+        assert torch.equal(b.matmul(x, out_dtype=torch.bfloat16), want)
+    # weights quantised in inference mode, and inputs made there, go on outside it
+    assert torch.equal(b.matmul(x, out_dtype=torch.bfloat16), want)
+    (dw,) = torch.autograd.grad(fp4.mx_linear(y, w[:, :40]), w, torch.ones(24, 40, dtype=torch.bfloat16, device="cuda"))
+    assert dw.shape == w.shape and not dw[:, 40:].any() and dw[:, :40].any()
+
+
+@pytest.mark.parametrize("how", ["recomputed", "recomputed, reentrant", "saved on the host"])
+def test_layer_under_checkpointing(how):
+    """What the layer saves are the transposed operands: made again, or brought back from the host, they are the same."""
+    from torch.utils.checkpoint import checkpoint
+    x = dense(70, 160, torch.bfloat16, 252).cuda().requires_grad_()
+    w = dense(96, 160, torch.float32, 253).cuda().requires_grad_()
+    g = dense(70, 96, torch.bfloat16, 254).cuda()
+    want = torch.autograd.grad(fp4.mx_linear(x, w), (x, w), g)
+    for _ in range(2):
+        x.grad = w.grad = None
+        if how == "saved on the host":
+            with torch.autograd.graph.save_on_cpu():
+                y = fp4.mx_linear(x, w)
+        else:
+            y = checkpoint(fp4.mx_linear, x, w, use_reentrant="reentrant" in how)
+        y.backward(g)
+        assert torch.equal(x.grad, want[0]) and torch.equal(w.grad, want[1])
+
+
+def test_layer_as_a_graphed_callable():
+    """Forward and backward captured by torch's own helper, replayed beside eager work."""
+    class Layer(torch.nn.Module):
+        def __init__(self):
+            super().__init__()
+            self.w = torch.nn.Parameter(dense(96, 512, torch.float32, 255))
+
+        def forward(self, x):
+            return fp4.mx_linear(x, self.w)
+
+    layer = Layer().cuda()
+    sample = dense(130, 512, torch.bfloat16, 256).cuda().requires_grad_()
+    plain = Layer().cuda()
+    graphed = torch.cuda.make_graphed_callables(layer, (sample,))
+    for i in range(4):
+        x = dense(130, 512, torch.bfloat16, 257 + i).cuda().requires_grad_()
+        g = dense(130, 96, torch.bfloat16, 267 + i).cuda()
+        y = graphed(x)
+        got = torch.autograd.grad(y, (x, layer.w), g)
+        torch.cuda.synchronize()
+        ye = fp4.mx_linear(x, plain.w)
+        want = torch.autograd.grad(ye, (x, plain.w), g)
+        assert torch.equal(y, ye) and all(torch.equal(a, b) for a, b in zip(got, want))
+        torch.cuda.synchronize()
