@@ -492,7 +492,8 @@ class MXTensor:
     @staticmethod
     def from_canonical(codes: torch.Tensor, scales: torch.Tensor, K: int | None = None) -> "MXTensor":
         """Codes [rows, K / 2] and E8M0 scales [rows, K / 32] as checkpoints hold them. The tensors are used as they are
-        where their rows are aligned (codes to 16 bytes, scales to 4), and copied otherwise."""
+        where their rows are aligned (codes to 16 bytes, scales to 4), and copied otherwise. K that is not a multiple of 32
+        leaves codes past K in each row's last block, which have to be zeros: products do not mask them."""
         return MXTensor(*_native.from_canonical(codes, scales, K))
 
     @staticmethod

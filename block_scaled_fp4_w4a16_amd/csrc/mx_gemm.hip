@@ -7,17 +7,21 @@
 // bits, so that the operand reads (16 rows, one block each) are as fast as reads of consecutive bytes: 1.75 ns per
 // instruction and compute unit; with rows 8 .. 15 swizzled differently from 0 .. 7 they take 3.5. The codes are MFMA
 // operands as they stand.
-// A wave holds one chunk's operands of both matrices and the next chunk's of B: after the MFMAs of row tile i it
-// reads row tile i of the next chunk into the registers just freed, so an operand is read about a chunk ahead. In a
-// stage's second chunk every LDS read of the stage has been issued, so the barrier that ends the stage stands at
-// that chunk's start and the matrix core works through the reads and loads behind it.
+// A wave holds the operands of two chunks of 128 positions, of both matrices, in two sets of registers. While one chunk's
+// MFMAs run from one set, the next chunk's operands are read into the other, B's first, dealt out behind the MFMAs of the
+// first three quarters of the row tiles. That set is free by then: the chunk before used it, and an MFMA issued in order
+// has taken its operands before a later read can return. In a stage's second chunk every LDS read of the stage has
+// been issued, so the barrier that ends the stage stands behind that chunk's first MFMA, and the matrix core works through
+// the reads and loads behind it.
 // Blocks past K: their scale bytes are replaced by 0 on both sides, which makes every product at most
 // 36 2^-254 = 0 in FP32, whatever the codes are. Rows past M or N load nothing and are not stored.
-// Tiles of 256 (64 KB of codes a stage, one workgroup per compute unit) are bound by power: 8192 x 14336 x 4096 takes 243 us,
-// 3.95 PFLOP/s; the same matrix instructions on random operands in registers alone reach 6.5 to 7.2 at 1.6 to 1.7 GHz.
+// Tiles of 256 (64 KB of codes a stage, one workgroup per compute unit): 8192 x 14336 x 4096 takes 240 us, 4.0 PFLOP/s, with
+// FP32 output 300 us (its epilogue spills). A stage takes 3350 to 3600 cycles against 2048 of matrix instructions, which
+// run for 47 % of the kernel's cycles at 2.1 GHz; the same instructions on random operands in registers alone reach 6.5
+// to 7.2 PFLOP/s at 1.6 to 1.7 GHz.
 // Smaller tiles are for fewer outputs and are bound by their loads: 16 KB a stage of 64 x 64 outputs take 0.26 us on a
-// compute unit (64 bytes per ns), 0.41 for two workgroups at once; 333 x 2560 x 9728 13.0 us, 64 x 14336 x 4096 8.1 us
-// (33 MB, 4.1 TB/s).
+// compute unit (64 bytes per ns), 0.41 for two workgroups at once; 333 x 2560 x 9728 13.3 us, 64 x 14336 x 4096 8.1 us
+// (33 MB, 4.1 TB/s), from weights that stay in the caches; 15.1 and 11.2 us from cold ones.
 #include "mx.h"
 #include "mx_plan.h"
 

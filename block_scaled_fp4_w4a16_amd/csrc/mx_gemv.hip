@@ -5,8 +5,9 @@
 // pairs of 128-position chunks (a pair is one 128-byte line of a weight row), which go through LDS in whole lines. A lane
 // reads 16-byte blocks of codes that are MFMA operands as they stand: nothing is decoded, and the scaled matrix
 // instruction applies the block scales. The waves' sums meet in LDS in a fixed order.
-// One row of 9728 x 2560 (13.2 MB) takes 4.3 us, 3.1 TB/s, of 8192 x 28672 (125 MB) 22.5 us, 5.5 TB/s: the small ones are
-// bound by a launch (1.8 us) and one round trip to memory.
+// One row of 9728 x 2560 (13.2 MB) takes 5.5 us from cold weights, 2.4 TB/s, of 8192 x 28672 (125 MB) 25.1 us, 5.0 TB/s, and 3.4
+// and 20.4 us where the same weights come again (replayed in a graph): the small ones are bound by a launch (1.8 us) and one
+// round trip to memory. The figures below are of weights that come again.
 #include "mx.h"
 
 namespace mx {

@@ -18,10 +18,10 @@ struct Plan {
   double us;   // what it is taken to cost
 };
 
-// What a tile costs, in microseconds as measured on 256 compute units: a launch with its first loads and last stores,
-// each further round's stores, and a stage of 256 positions with one workgroup on a unit (256: with every unit busy; a
-// few workgroups of 256 run a stage in 1.2) and with two (64 and 128: two fit; their stages run at 16 and 28 outputs per
-// nanosecond, those of 256 at 37).
+// What a tile costs, in microseconds as measured on 256 compute units with 16-bit outputs and operands that come again (those
+// of a few MB from the caches): a launch with its first loads and last stores, each further round's stores, and a stage of
+// 256 positions with one workgroup on a unit (256: with every unit busy; a few workgroups of 256 run a stage in 1.2) and
+// with two (64 and 128: two fit; their stages run at 16 and 28 outputs per nanosecond, those of 256 at 37).
 struct TileCost {
   int tile;
   double launch, round, one, two;
@@ -48,7 +48,8 @@ inline Plan plan_of(int64_t M, int64_t N, int64_t K, int cus, bool split = true)
   p.per = (stages + 1) & ~1;
   p.us = 1e30;
   // up to 16 rows: rows_kernel, by its chunk pairs and tiles of 16 (4096 x 4096 at M = 1 and 16: 2.8 and 3.2 us, tiles of 64
-  // 7.2; 28672 x 8192: 26.4 and 31.9 us against 25.9 and 27.0)
+  // 7.2; 28672 x 8192: 26.4 and 31.9 us against 25.9 and 27.0). The figure takes the work as spread over the device; few
+  // columns with a long K take longer (1 x 16 x 2^20: 216 us, where 17 rows in K parts take 70; 16 x 128 x 65536: 16.8, 12.7)
   if (M <= 16) p.us = 1.8 + (double)((N + 15) / 16) * stages * (0.00034 + 0.00001 * M);
   const double least = 3.5 + N * K * (17 / 32.) / 5e6;  // the weights' bytes at 5 TB/s
   for (const TileCost& c : TILE_COSTS) {
@@ -78,9 +79,9 @@ inline Plan plan_of(int64_t M, int64_t N, int64_t K, int cus, bool split = true)
 inline int64_t plane_bytes(const Plan& p, int64_t M) { return p.parts > 1 ? p.parts * M * p.ldp * 4 : 0; }
 
 // Whether dense activations are quantised inside the product, else into the workspace before it. Each workgroup of 16
-// weight rows then quantises all of them again, which pays while rows and rounds are few: 4096 x 4096 at M = 1, 4 and 8 takes
-// 4.2, 4.6 and 5.3 us against 4.8, 4.9 and 5.1 in two kernels, 9728 x 2560 at M = 1 and 4 5.9 and 6.7 against 6.4 and 6.8,
-// 14336 x 4096 at M = 1 12.3 against 9.5.
+// weight rows then quantises all of them again, which pays while rows and rounds are few. With weights that come again, 4096 x
+// 4096 at M = 1, 4 and 8 takes 4.2, 4.6 and 5.3 us against 4.8, 4.9 and 5.1 in two kernels, 9728 x 2560 at M = 1 and 4 5.9 and
+// 6.7 against 6.4 and 6.8, 14336 x 4096 at M = 1 12.3 against 9.5.
 inline bool fused(int64_t M, int64_t N, int64_t K) {
   return M <= 16 && (N + 15) / 16 * stages_of(K) * (M + 3) <= 32768;
 }
