@@ -43,7 +43,26 @@ class Mx(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("s", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("lds", ctypes.c_int64)]
 
 
+class Epilogue(ctypes.Structure):
+    """Mirror of `fp4_epilogue` (what follows an MXFP4 product)."""
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("z", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("ldz", ctypes.c_int64), ("bias_type", ctypes.c_int), ("residual_type", ctypes.c_int), ("activation", ctypes.c_int)]
+
+
+class Groups(ctypes.Structure):
+    """Mirror of `fp4_groups` (rows in groups, one per expert)."""
+    _fields_ = [("offsets", ctypes.c_void_p), ("count", ctypes.c_int64), ("bits", ctypes.c_int)]
+
+
+class Gradient(ctypes.Structure):
+    """Mirror of `fp4_gradient` (a gradient's way back through an epilogue)."""
+    _fields_ = [("z", ctypes.c_void_p), ("dbias", ctypes.c_void_p), ("ldz", ctypes.c_int64), ("activation", ctypes.c_int),
+                ("dbias_type", ctypes.c_int)]
+
+
 _mx = ctypes.POINTER(Mx)
+_epi = ctypes.POINTER(Epilogue)
+_groups = ctypes.POINTER(Groups)
 _SIGS = {
     "fp4_abi_version": (_c, []),
     "fp4_status_string": (ctypes.c_char_p, [_c]),
@@ -69,6 +88,16 @@ _SIGS = {
     "w4a4_matmul_workspace_bytes": (_i64, [_i64, _i64, _i64]),
     "w4a4_linear": (_c, [_c, _c, _i64, _i64, _i64, _p, _i64, _mx, _p, _i64, _p, ctypes.c_size_t, _p]),
     "w4a4_linear_workspace_bytes": (_i64, [_i64, _i64, _i64]),
+    "w4a4_matmul_epilogue": (_c, [_c, _i64, _i64, _i64, _mx, _mx, _epi, _p, _i64, _p, ctypes.c_size_t, _p]),
+    "w4a4_linear_epilogue": (_c, [_c, _c, _i64, _i64, _i64, _p, _i64, _mx, _epi, _p, _i64, _p, ctypes.c_size_t, _p]),
+    "w4a4_grouped_matmul": (_c, [_c, _i64, _i64, _i64, _groups, _mx, _mx, _epi, _c, _p, _i64, _p]),
+    "w4a4_grouped_linear": (_c, [_c, _c, _i64, _i64, _i64, _groups, _p, _i64, _mx, _epi, _c, _p, _i64, _p, ctypes.c_size_t, _p]),
+    "w4a4_grouped_linear_workspace_bytes": (_i64, [_i64, _i64, _i64, _i64]),
+    "fp4_grouped_depth": (_i64, [_i64, _i64]),
+    "fp4_grouped_sums_bytes": (_i64, [_i64, _i64, _i64]),
+    "fp4_quantize_mxfp4_grouped": (_c, [_c, _i64, _i64, _p, _i64, _groups, _mx, _mx, ctypes.POINTER(Gradient), _p, ctypes.c_size_t, _p]),
+    "w4a4_grouped_gradient": (_c, [_c, _i64, _i64, _i64, _groups, _mx, _mx, _p, _i64, _p]),
+    "w4a4_grouped_matmul_t": (_c, [_c, _i64, _i64, _i64, _groups, _mx, _mx, _c, _p, _i64, _p]),
 }
 
 _lib = None
@@ -456,16 +485,42 @@ def w4a4_linear_workspace_bytes(M, N, K, device=None) -> int:
     return _mx_workspace_bytes("w4a4_linear_workspace_bytes", M, N, K, device)
 
 
-def w4a4_matmul(M, N, K, aq, a_s, bq, bs, y, stream=None, workspace=None):
-    """y [M, N] (float32, bfloat16 or float16; rows may be strided) = A B^T of two MXFP4 operands of depth K.
+def w4a4_matmul(M, N, K, aq, a_s, bq, bs, y, stream=None, workspace=None, bias=None, activation=None, residual=None):
+    """y [M, N] (float32, bfloat16 or float16; rows may be strided) = f(A B^T + bias) + residual of two MXFP4 operands of depth
+    K, rounded once. bias [N], residual [M, N] (float32, bfloat16 or float16; it may be y itself) and the activation f, None,
+    "relu", "silu", "gelu" or "gelu_tanh", are each left out by default.
     `workspace`: a uint8 CUDA tensor, by default one of the size the library asks for, allocated here."""
-    _native.matmul(M, N, K, aq, a_s, bq, bs, y, stream, workspace)
+    _native.matmul(M, N, K, aq, a_s, bq, bs, y, stream, workspace, bias, activation, residual)
 
 
-def w4a4_linear(M, N, K, x, bq, bs, y, stream=None, workspace=None):
-    """y [M, N] = Q(x) B^T: dense x [M, K] quantised along its rows, times an MXFP4 operand of depth K. No
-    gradient is computed: x or y that requires one is refused while gradients are enabled."""
-    _native.linear(M, N, K, x, bq, bs, y, stream, workspace)
+def w4a4_linear(M, N, K, x, bq, bs, y, stream=None, workspace=None, bias=None, activation=None, residual=None):
+    """y [M, N] = f(Q(x) B^T + bias) + residual: dense x [M, K] quantised along its rows, times an MXFP4 operand of depth K;
+    what follows as in w4a4_matmul. No gradient is computed: tensors that require one are refused while gradients are enabled."""
+    _native.linear(M, N, K, x, bq, bs, y, stream, workspace, bias, activation, residual)
+
+
+def w4a4_grouped_linear_workspace_bytes(T, N, K, count, device=None) -> int:
+    """Workspace bytes of w4a4_grouped_linear for this shape and number of groups on `device` (default: the current one)."""
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        n = int(lib().w4a4_grouped_linear_workspace_bytes(T, N, K, count))
+    _check(n if n < 0 else 0, "w4a4_grouped_linear_workspace_bytes")
+    return n
+
+
+def w4a4_grouped_matmul(T, N, K, aq, a_s, bq, bs, offsets, y, bias=None, activation=None, residual=None, fill=False, stream=None):
+    """Rows in groups (experts): y[t] = f(A[t] B_e^T + bias[e]) + residual[t] for the rows t in offsets[e] .. offsets[e + 1] - 1.
+
+    A has T rows, B N rows for each expert, one expert after the other; offsets: E + 1 bounds that grow from 0 or more to at
+    most T (int32 or int64, on the GPU: the host never learns the sizes; groups may be empty, E is at most 512). bias [E, N];
+    residual, activation and y as in w4a4_matmul. Rows of no group, in front of the first bound and behind the last, are left
+    as they are in y, or, with `fill`, become the residual (zero without one)."""
+    _native.grouped_matmul(T, N, K, aq, a_s, bq, bs, offsets, y, bias, activation, residual, fill, stream)
+
+
+def w4a4_grouped_linear(T, N, K, x, bq, bs, offsets, y, bias=None, activation=None, residual=None, fill=False, stream=None, workspace=None):
+    """w4a4_grouped_matmul of dense x [T, K], quantised along its rows on the way. No gradient is computed: tensors that require
+    one are refused while gradients are enabled."""
+    _native.grouped_linear(T, N, K, x, bq, bs, offsets, y, bias, activation, residual, fill, stream, workspace)
 
 
 @dataclass
@@ -518,24 +573,61 @@ class MXTensor:
         return _native.dequant_new(self.codes, self.scales, self.rows, self.K, dtype, stream)
 
     def matmul(self, x, out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
-               stream=None, workspace: torch.Tensor | None = None) -> torch.Tensor:
-        """x self^T [M, rows], self the weights: x an MXTensor of the same K, or dense [M, K], quantised on the way. No
-        gradient is computed: dense x (or `out`) that requires one is refused while gradients are enabled."""
+               stream=None, workspace: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+               activation: str | None = None, residual: torch.Tensor | None = None) -> torch.Tensor:
+        """f(x self^T + bias) + residual [M, rows], self the weights: x an MXTensor of the same K, or dense [M, K], quantised on
+        the way; bias [rows], activation and residual [M, rows] (which may be `out`) as in w4a4_matmul, in the product's own
+        kernels. No gradient is computed: dense x, bias or residual (or `out`) that requires one is refused while gradients
+        are enabled."""
         if isinstance(x, MXTensor):
             if x.K != self.K:
                 raise ValueError(f"depths differ: {x.K} and {self.K}")
             return _native.matmul_new(x.codes, x.scales, x.rows, self.codes, self.scales, self.rows, self.K, out, out_dtype,
-                                      stream, workspace)
-        return _native.linear_new(x, self.codes, self.scales, self.rows, self.K, out, out_dtype, stream, workspace)
+                                      stream, workspace, bias, activation, residual)
+        return _native.linear_new(x, self.codes, self.scales, self.rows, self.K, out, out_dtype, stream, workspace, bias, activation,
+                                  residual)
+
+    def grouped_matmul(self, x, offsets: torch.Tensor, out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
+                       stream=None, workspace: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                       activation: str | None = None, residual: torch.Tensor | None = None) -> torch.Tensor:
+        """The products of experts, self their weights one after the other (MXTensor.quantize of [E, N, K] makes them): row t of x
+        (an MXTensor, or dense [T, K]) in offsets[e] .. offsets[e + 1] - 1 takes expert e's N rows; see w4a4_grouped_matmul.
+        Rows of no group are the residual, or zero, in a result made here, and left as they are in `out`. `workspace` is
+        taken for dense x only."""
+        if isinstance(x, MXTensor):
+            if x.K != self.K:
+                raise ValueError(f"depths differ: {x.K} and {self.K}")
+            return _native.grouped_matmul_new(x.codes, x.scales, x.rows, self.codes, self.scales, self.rows, self.K, offsets, out,
+                                              out_dtype, stream, bias, activation, residual)
+        return _native.grouped_linear_new(x, self.codes, self.scales, self.rows, self.K, offsets, out, out_dtype, stream, workspace, bias,
+                                          activation, residual)
 
 
-def mx_linear(x: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
-    """x [..., K] times w [N, K] transposed, both quantised to MXFP4 in the call, in x's type; differentiable once in both.
+def mx_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, activation: str | None = None,
+              residual: torch.Tensor | None = None) -> torch.Tensor:
+    """f(x w^T + bias) + residual: x [..., K] times w [N, K] transposed, both quantised to MXFP4 in the call, in x's type, rounded
+    once; differentiable once in all of them. bias [N], the activation f (None, "relu", "silu", "gelu" or "gelu_tanh") and
+    residual (of the result's shape) are each left out by default.
 
     Rounding to MXFP4 counts as the identity in the backward pass, whose products are MXFP4 too: with g the gradient of
     the result, dx = Q(g) Q(w^T)^T in x's type and dw = Q(g^T) Q(x^T)^T in w's, every operand quantised along the axis that
-    its product contracts. x and w are float32, bfloat16 or float16 on one GPU.
+    its product contracts. With an activation, D = g f'(x w^T + bias), in g's type, takes g's place (as in the gradient of the
+    activation as a layer of its own), the sum in f' being kept in float32 from the forward pass. The bias's gradient is the
+    sum of g f' over the rows, from its float32 values; the residual's is g. x, w, bias and residual are float32, bfloat16 or
+    float16 on one GPU.
 
     A step captured into a graph takes its gradients with torch.autograd.grad; torch's accumulation into `.grad` joins the
     stream on which an eager step that is still alive first used the leaf, which a capture cannot do."""
-    return _native.mx_linear(x, w)
+    return _native.mx_linear(x, w, bias, activation, residual)
+
+
+def mx_grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, bias: torch.Tensor | None = None,
+                      activation: str | None = None, residual: torch.Tensor | None = None) -> torch.Tensor:
+    """mx_linear for experts: the rows of x [..., K] (counted over all axes but the last) from offsets[e] to offsets[e + 1] - 1 are
+    multiplied by w[e] of w [E, N, K] and take bias[e] of bias [E, N]; differentiable once in x, w, bias and residual.
+
+    offsets: E + 1 bounds (int32 or int64) that grow from 0 or more to at most the number of rows, on the GPU: nothing waits for
+    their values. Rows of no expert have no product: the result there is the residual, or zero, and so is x's gradient zero.
+    An expert without rows has zero gradients. Blocks of the operands that the weights' gradients contract begin anew at
+    each expert's first row. Otherwise as mx_linear."""
+    return _native.mx_grouped_linear(x, w, offsets, bias, activation, residual)

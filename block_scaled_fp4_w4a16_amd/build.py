@@ -17,7 +17,7 @@ PROBE_LIB = os.path.join(HERE, "libfp4probe.so")
 PROBE_SOURCES = ["probe.hip"]
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "layout.hip", "gemv.hip", "gemm.hip", "quantize.hip",
-           "mx_quant.hip", "mx_gemv.hip", "mx_gemm.hip"]
+           "mx_quant.hip", "mx_gemv.hip", "mx_gemm.hip", "mx_epilogue.hip", "mx_grouped.hip", "mx_segments.hip"]
 ARCH = os.environ.get("FP4_OFFLOAD_ARCH", "gfx950")
 
 FLAGS = [

@@ -156,12 +156,37 @@ static inline int check_dims(int64_t rows, int64_t k) {
   return FP4_OK;
 }
 
+static inline int check_product(int out_type, int64_t M, int64_t N, int64_t K) {
+  if (!valid_type(out_type)) return FP4_ERR_ARG;
+  if (N < 1) return FP4_ERR_SHAPE;
+  if (int rc = check_dims(M, K)) return rc;
+  if (N > MAX_ROWS) return FP4_ERR_UNSUPPORTED;
+  return FP4_OK;
+}
+
+static inline int check_output(int out_type, int64_t N, const void* y, int64_t ldy) {
+  if (!y) return FP4_ERR_ARG;
+  if (ldy < N) return FP4_ERR_SHAPE;
+  if (ldy > (1LL << 40)) return FP4_ERR_UNSUPPORTED;
+  return fp4_aligned(y, (uintptr_t)elem_bytes(out_type)) ? FP4_OK : FP4_ERR_ALIGN;
+}
+
+// Dense activations x[M][K] (M at least 1).
+static inline int check_dense(int type, int64_t K, const void* x, int64_t ldx) {
+  if (!x) return FP4_ERR_ARG;
+  if (ldx < K) return FP4_ERR_SHAPE;
+  if (ldx > (1LL << 40)) return FP4_ERR_UNSUPPORTED;
+  return fp4_aligned(x, (uintptr_t)elem_bytes(type)) ? FP4_OK : FP4_ERR_ALIGN;
+}
+
 // Whether a launch stays below the 2^32 work items that one can have.
 static inline bool fits_launch(int64_t workgroups, int threads) { return workgroups * threads < (1LL << 32); }
 
 // Products of already checked arguments (mx_gemv.hip, mx_gemm.hip).
 int launch_rows(int x_type, int out_type, int M, int N, int K, const void* x, int64_t ldx, const fp4_mx* a,
-                const fp4_mx& b, void* y, int64_t ldy, hipStream_t st);
+                const fp4_mx& b, void* y, int64_t ldy, hipStream_t st, const fp4_epilogue* epi = nullptr);
+int launch_planes(int tile, int parts, int per, int64_t ldp, int M, int N, int K, const fp4_mx& a, const fp4_mx& b, void* planes,
+                  hipStream_t st);
 int launch_quantize_rows(int type, int64_t M, int64_t K, const void* x, int64_t ldx, const fp4_mx& rows, hipStream_t st);
 
 }  // namespace mx

@@ -8,7 +8,8 @@
 // One row of 9728 x 2560 (13.2 MB) takes 5.5 us from cold weights, 2.4 TB/s, of 8192 x 28672 (125 MB) 25.1 us, 5.0 TB/s, and 3.4
 // and 20.4 us where the same weights come again (replayed in a graph): the small ones are bound by a launch (1.8 us) and one
 // round trip to memory. The figures below are of weights that come again.
-#include "mx.h"
+#include "mx_epilogue.h"
+#include "mx_groups.h"
 
 namespace mx {
 
@@ -91,23 +92,20 @@ __device__ __forceinline__ u32x4 read_block(const uint8_t* codes, int n, int g, 
 constexpr int GV_W = 0, GV_WS = 2048, GV_AS = 2304, GV_A = 2560;
 static __host__ __device__ __forceinline__ int wave_lds(bool dense, int M) { return dense ? GV_AS : M <= 8 ? GV_A + 1024 : GV_A + 2048; }
 
+// The sums of 16 columns from n0 on, in the first wave: lane l = 16 g + n has row n, columns n0 + 4 g .. + 3.
 // XT: 0 for A in MXFP4, else the type of dense A. A wave takes the pairs wave, wave + waves, ... one after the other: loads
 // of several pairs at once, or of the next one ahead, took as long or longer at every size (the waves of a compute unit
-// cover each other). The arguments that the weights' loads need come first: they are preloaded into scalar registers.
+// cover each other). `each`: LDS bytes of a wave; A of `half` has 8 rows there.
 template <int XT>
-__global__ void __launch_bounds__(64 * GV_MAX_WAVES)
-    rows_kernel(const uint8_t* __restrict__ bq, const uint8_t* __restrict__ bs, int N, int K, int ldq, int lds, int m_waves,
-                const void* __restrict__ a, const uint8_t* __restrict__ as, int64_t lda, int las, void* __restrict__ y,
-                int64_t ldy, int out_type, int vec) {
-  extern __shared__ uint8_t space[];
-  const int lane = threadIdx.x & 63, waves = m_waves >> 8, M = m_waves & 255;
+__device__ __forceinline__ f32x4 rows_sum(uint8_t* space, int each, bool half, int waves, int n0, const uint8_t* bq, const uint8_t* bs,
+                                          int N, int K, int ldq, int lds, int M, const void* a, const uint8_t* as, int64_t lda, int las) {
+  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int nb = (int)blocks_of(K), pairs = (nb + 7) >> 3;
-  const int n0 = blockIdx.x * 16, rows = min(16, N - n0);
+  const int rows = min(16, N - n0);
   const auto wq = fp4::make_rsrc(bq + (int64_t)n0 * ldq, (uint32_t)((rows - 1) * ldq + nb * BLOCK_BYTES));
   const auto ws = fp4::make_rsrc(bs + (int64_t)n0 * lds, (uint32_t)((rows - 1) * lds + ((nb + 3) & ~3)));
-  const int each = wave_lds(XT != 0, M);
   uint8_t* const mine = space + wave * each;
 
   f32x4 acc = {0, 0, 0, 0};
@@ -120,7 +118,7 @@ __global__ void __launch_bounds__(64 * GV_MAX_WAVES)
       // rows of A past M: what is there, for sums that are not stored
       const auto aq = fp4::make_rsrc(a, (uint32_t)((M - 1) * (int)lda + nb * BLOCK_BYTES));
       const auto ar = fp4::make_rsrc(as, (uint32_t)((M - 1) * las + ((nb + 3) & ~3)));
-      load_pair(aq, ar, (int)lda, las, p, M <= 8, mine + GV_A, mine + GV_AS, lane);
+      load_pair(aq, ar, (int)lda, las, p, half, mine + GV_A, mine + GV_AS, lane);
     } else {
       const uint8_t* row = static_cast<const uint8_t*>(a) + (int64_t)min(n, M - 1) * lda * elem_bytes(XT);
 #pragma unroll
@@ -130,7 +128,7 @@ __global__ void __launch_bounds__(64 * GV_MAX_WAVES)
     asm volatile("" ::: "memory");
     const u32x2 wsc = *reinterpret_cast<const u32x2*>(mine + GV_WS + n * 8);
     if constexpr (XT == 0) {
-      const int an = M <= 8 ? n & 7 : n;
+      const int an = half ? n & 7 : n;
       const u32x2 s = *reinterpret_cast<const u32x2*>(mine + GV_AS + n * 8);
       av[0] = read_block(mine + GV_A, an, g, 0);
       av[1] = read_block(mine + GV_A, an, g, 1);
@@ -149,38 +147,146 @@ __global__ void __launch_bounds__(64 * GV_MAX_WAVES)
 
   *reinterpret_cast<f32x4*>(mine + lane * 16) = acc;
   __syncthreads();
-  if (threadIdx.x < 64) {
-    f32x4 sum = acc;
+  f32x4 sum = acc;
+  if (threadIdx.x < 64)
     for (int v = 1; v < waves; ++v) sum += *reinterpret_cast<const f32x4*>(space + v * each + lane * 16);
-    const int c = n0 + 4 * g;
-    if (n < M && c < N) store4(out_type, y, n * ldy + c, sum, N - c, vec);
-  }
+  return sum;
 }
 
+// The arguments that the weights' loads need come first: they are preloaded into scalar registers.
 template <int XT>
-static int launch_variant(int waves, int out_type, int M, int N, int K, const void* x, int64_t ldx, const fp4_mx* a,
-                          const fp4_mx& b, void* y, int64_t ldy, hipStream_t st) {
-  const int eb = elem_bytes(out_type);
-  const int vec = fp4_aligned(y, 4 * eb) && ldy % 4 == 0;
-  const dim3 grid((unsigned)((N + 15) / 16));
-  if (!fits_launch(grid.x, 64 * waves)) return FP4_ERR_UNSUPPORTED;
-  return fp4_launch(rows_kernel<XT>, grid, dim3(64 * waves), (size_t)waves * wave_lds(XT != 0, M), st, b.q, b.s, N, K, b.ldq, b.lds,
-                    M | waves << 8, XT ? x : a->q, XT ? nullptr : a->s, XT ? ldx : a->ldq, XT ? 0 : a->lds, y, ldy, out_type, vec);
+__global__ void __launch_bounds__(64 * GV_MAX_WAVES)
+    rows_kernel(const uint8_t* __restrict__ bq, const uint8_t* __restrict__ bs, int N, int K, int ldq, int lds, int m_waves,
+                const void* __restrict__ a, const uint8_t* __restrict__ as, int64_t lda, int las, void* __restrict__ y,
+                int64_t ldy, int out_type, int vec) {
+  extern __shared__ uint8_t space[];
+  const int waves = m_waves >> 8, M = m_waves & 255, n0 = blockIdx.x * 16;
+  const f32x4 sum = rows_sum<XT>(space, wave_lds(XT != 0, M), M <= 8, waves, n0, bq, bs, N, K, ldq, lds, M, a, as, lda, las);
+  const int lane = threadIdx.x, n = lane & 15, c = n0 + 4 * (lane >> 4);
+  if (threadIdx.x < 64 && n < M && c < N) store4(out_type, y, n * ldy + c, sum, N - c, vec);
+}
+
+// The same with an epilogue.
+template <int XT>
+__global__ void __launch_bounds__(64 * GV_MAX_WAVES)
+    rows_epilogue_kernel(const uint8_t* __restrict__ bq, const uint8_t* __restrict__ bs, int N, int K, int ldq, int lds, int m_waves,
+                         const void* a, const uint8_t* as, int64_t lda, int las, void* y, int64_t ldy, int out_type, fp4_epilogue epi) {
+  extern __shared__ uint8_t space[];
+  const int waves = m_waves >> 8, M = m_waves & 255, n0 = blockIdx.x * 16;
+  const f32x4 sum = rows_sum<XT>(space, wave_lds(XT != 0, M), M <= 8, waves, n0, bq, bs, N, K, ldq, lds, M, a, as, lda, las);
+  const int lane = threadIdx.x, n = lane & 15, c = n0 + 4 * (lane >> 4);
+  if (threadIdx.x < 64 && n < M && c < N) finish4(epi, out_type, y, ldy, n, c, c, sum, N - c);
+}
+
+// Up to 16 rows in groups, each with rows of B and a bias of its own. Workgroups in y take the groups that have rows, in order
+// (as many as there are rows at most); those past the last one leave.
+template <int XT>
+__global__ void __launch_bounds__(64 * GV_MAX_WAVES)
+    rows_grouped_kernel(const uint8_t* __restrict__ bq, const uint8_t* __restrict__ bs, int N, int K, int ldq, int lds, int m_waves,
+                        Groups groups, int64_t step_q, int64_t step_s, const void* a, const uint8_t* as, int64_t lda, int las, void* y,
+                        int64_t ldy, int out_type, int fill, fp4_epilogue epi) {
+  extern __shared__ uint8_t space[];
+  const int waves = m_waves >> 8, T = m_waves & 255, n0 = blockIdx.x * 16;
+  const int lane = threadIdx.x & 63;
+  int seen = 0, most = 0, first = 0, e = -1, row0 = 0, M = 0;
+  for (int base = 0; base < groups.E; base += 64) {
+    // bounds that decrease count as the largest in front of them (read_groups)
+    const int i = base + lane;
+    int lo = i < groups.E ? bound_at(groups, i, T) : 0, hi = i < groups.E ? bound_at(groups, i + 1, T) : 0;
+    if (base == 0) first = uniform(lo);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int l = __shfl_up(lo, d), h = __shfl_up(hi, d);
+      if (lane >= d) lo = max(lo, l), hi = max(hi, h);
+    }
+    lo = max(lo, most), hi = max(max(hi, lo), most);
+    const bool here = i < groups.E && hi > lo;
+    const uint64_t some = __builtin_amdgcn_ballot_w64(here);
+    const int rank = seen + __builtin_popcountll(some & ((1ull << lane) - 1));
+    const uint64_t mine = __builtin_amdgcn_ballot_w64(here && rank == (int)blockIdx.y);
+    if (mine) {
+      const int from = __builtin_ctzll(mine);
+      e = base + from;
+      row0 = __builtin_amdgcn_readlane(lo, from), M = __builtin_amdgcn_readlane(hi, from) - row0;
+    }
+    seen += __builtin_popcountll(some);
+    most = __builtin_amdgcn_readlane(hi, 63);
+  }
+  if (fill && blockIdx.y == 0 && (int)threadIdx.x < 256) {
+    const int r = threadIdx.x >> 4, c = n0 + (threadIdx.x & 15);
+    if (r < first + T - most && c < N) {
+      const int64_t row = row_outside(r, first, most);
+      float f[1] = {0};
+      if (epi.residual) values_of(epi.residual_type, load_raw<1>(epi.residual_type, epi.residual, row * epi.ldr + c, 1), f);
+      store_values(out_type, y, row * ldy + c, f, 1);
+    }
+  }
+  if (M == 0) return;
+  const uint8_t* const ar = static_cast<const uint8_t*>(a) + (int64_t)row0 * lda * (XT == 0 ? 1 : elem_bytes(XT));
+  const f32x4 sum = rows_sum<XT>(space, wave_lds(XT != 0, T), T <= 8, waves, n0, bq + e * step_q, bs + e * step_s, N, K, ldq, lds, M, ar,
+                                 as + (int64_t)row0 * las, lda, las);
+  const int n = lane & 15, c = n0 + 4 * (lane >> 4);
+  if (threadIdx.x < 64 && n < M && c < N)
+    finish4(epi, out_type, y, ldy, row0 + n, c, (int64_t)e * N + c, sum, N - c);
+}
+
+// A product of few rows: what launch_rows takes, and what comes behind the sums.
+struct Rows {
+  int x_type, out_type, M, N, K;
+  const void* x;
+  int64_t ldx;
+  const fp4_mx* a;
+  const fp4_mx& b;
+  void* y;
+  int64_t ldy;
+  const fp4_epilogue* epi;
+  const Groups* groups;
+  int64_t step_q, step_s;
+  int fill;
+};
+
+template <int XT>
+static int launch_variant(const Rows& r, int waves, hipStream_t st) {
+  const int eb = elem_bytes(r.out_type), m_waves = r.M | waves << 8;
+  const int vec = fp4_aligned(r.y, 4 * eb) && r.ldy % 4 == 0;
+  const dim3 grid((unsigned)((r.N + 15) / 16), r.groups ? (unsigned)(r.M < r.groups->E ? r.M : r.groups->E) : 1), block(64 * waves);
+  if (!fits_launch((int64_t)grid.x * grid.y, 64 * waves)) return FP4_ERR_UNSUPPORTED;
+  const size_t lds = (size_t)waves * wave_lds(XT != 0, r.M);
+  const void *x = XT ? r.x : r.a->q, *s = XT ? nullptr : r.a->s;
+  const int64_t ldx = XT ? r.ldx : r.a->ldq, las = XT ? 0 : r.a->lds;
+  if (r.groups)
+    return fp4_launch(rows_grouped_kernel<XT>, grid, block, lds, st, r.b.q, r.b.s, r.N, r.K, r.b.ldq, r.b.lds, m_waves, *r.groups,
+                      r.step_q, r.step_s, x, s, ldx, las, r.y, r.ldy, r.out_type, r.fill, r.epi ? *r.epi : fp4_epilogue{});
+  if (r.epi)
+    return fp4_launch(rows_epilogue_kernel<XT>, grid, block, lds, st, r.b.q, r.b.s, r.N, r.K, r.b.ldq, r.b.lds, m_waves, x, s, ldx, las,
+                      r.y, r.ldy, r.out_type, *r.epi);
+  return fp4_launch(rows_kernel<XT>, grid, block, lds, st, r.b.q, r.b.s, r.N, r.K, r.b.ldq, r.b.lds, m_waves, x, s, ldx, las, r.y, r.ldy,
+                    r.out_type, vec);
+}
+
+static int launch_any_rows(const Rows& r, hipStream_t st) {
+  const int pairs = (int)((blocks_of(r.K) + 7) / 8);
+  const int64_t tiles = (int64_t)((r.N + 15) / 16) * (r.groups ? (r.M < r.groups->E ? r.M : r.groups->E) : 1);
+  // Ten waves where a compute unit gets one workgroup (2560 x 9728: 4.7 us, with 8 waves 5.4; 4096 x 4096: 2.8 and 3.0),
+  // eight where it gets several, of which more then fit (9728 x 2560: 4.3 us, with 10 waves 4.6; 8192 x 28672: 22.5 and 23.8).
+  const int most = tiles > fp4_device_cus() ? 8 : 10, waves = pairs < most ? pairs : most;
+  if (r.x_type == FP4_TYPE_F32) return launch_variant<FP4_TYPE_F32>(r, waves, st);
+  if (r.x_type == FP4_TYPE_BF16) return launch_variant<FP4_TYPE_BF16>(r, waves, st);
+  if (r.x_type == FP4_TYPE_F16) return launch_variant<FP4_TYPE_F16>(r, waves, st);
+  return launch_variant<0>(r, waves, st);
 }
 
 // M <= 16.
 int launch_rows(int x_type, int out_type, int M, int N, int K, const void* x, int64_t ldx, const fp4_mx* a,
-                const fp4_mx& b, void* y, int64_t ldy, hipStream_t st) {
-  const int pairs = (int)((blocks_of(K) + 7) / 8);
-  // Ten waves where a compute unit gets one workgroup (2560 x 9728: 4.7 us, with 8 waves 5.4; 4096 x 4096: 2.8 and 3.0),
-  // eight where it gets several, of which more then fit (9728 x 2560: 4.3 us, with 10 waves 4.6; 8192 x 28672: 22.5 and 23.8).
-  const int most = (N + 15) / 16 > fp4_device_cus() ? 8 : 10, waves = pairs < most ? pairs : most;
-#define MX_GV(XT) return launch_variant<XT>(waves, out_type, M, N, K, x, ldx, a, b, y, ldy, st)
-  if (x_type == FP4_TYPE_F32) MX_GV(FP4_TYPE_F32);
-  if (x_type == FP4_TYPE_BF16) MX_GV(FP4_TYPE_BF16);
-  if (x_type == FP4_TYPE_F16) MX_GV(FP4_TYPE_F16);
-  MX_GV(0);
-#undef MX_GV
+                const fp4_mx& b, void* y, int64_t ldy, hipStream_t st, const fp4_epilogue* epi) {
+  return launch_any_rows({x_type, out_type, M, N, K, x, ldx, a, b, y, ldy, epi, nullptr, 0, 0, 0}, st);
+}
+
+// The same with the rows in groups.
+int launch_rows_grouped(int x_type, int out_type, int T, int N, int K, const Groups& groups, const void* x, int64_t ldx, const fp4_mx* a,
+                        const fp4_mx& b, int64_t step_q, int64_t step_s, const fp4_epilogue* epi, void* y, int64_t ldy, int fill,
+                        hipStream_t st) {
+  return launch_any_rows({x_type, out_type, T, N, K, x, ldx, a, b, y, ldy, epi, &groups, step_q, step_s, fill}, st);
 }
 
 }  // namespace mx

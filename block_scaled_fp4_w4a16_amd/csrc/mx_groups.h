@@ -1,0 +1,95 @@
+// Rows in groups (one per expert) whose bounds lie in device memory: reading them, and finding a tile's group.
+#pragma once
+#include "mx.h"
+
+namespace mx {
+
+constexpr int MAX_GROUPS = 512;
+constexpr int UNIT = 256;  // positions that every group's part of an operand along the rows is padded to: a stage of the tiles
+
+// Group e's rows are [start[e], start[e + 1]). `offsets` null: `each` rows per group.
+struct Groups {
+  const void* offsets;
+  int E, wide;  // wide: 64-bit offsets
+  int each;
+};
+
+// Tables in LDS: start[E + 1], and units[E + 1] with the tiles of `unit` rows in front of each group.
+constexpr int group_table_bytes(int E) { return (2 * (E + 1) * 4 + 15) & ~15; }
+
+// Bound e of the groups, in [0, T]: whatever the memory holds, no row past T belongs to a group.
+__device__ __forceinline__ int bound_at(const Groups& g, int e, int T) {
+  int64_t v;
+  if (!g.offsets) v = (int64_t)e * g.each;
+  else v = g.wide ? static_cast<const int64_t*>(g.offsets)[e] : static_cast<const int32_t*>(g.offsets)[e];
+  return (int)(v < 0 ? 0 : v > T ? T : v);
+}
+
+// Fills the tables (one wave; the caller's barrier makes them visible). Bounds that decrease count as the largest in front of
+// them, so that groups never overlap and their rows are T at most.
+template <int UNIT_ROWS>
+__device__ __forceinline__ void read_groups(const Groups& g, int T, int* start, int* units, int lane) {
+  int most = 0, sum = 0, last = 0;
+  for (int base = 0; base <= g.E; base += 64) {
+    const int e = base + lane;
+    int v = e <= g.E ? bound_at(g, e, T) : 0;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int o = __shfl_up(v, d);
+      if (lane >= d) v = max(v, o);
+    }
+    v = max(v, most);
+    // the units of group e - 1, which ends here; the first lane's began in the 64 bounds before
+    int before = __shfl_up(v, 1);
+    if (lane == 0) before = base ? last : v;
+    int n = (v - before + UNIT_ROWS - 1) / UNIT_ROWS;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int o = __shfl_up(n, d);
+      if (lane >= d) n += o;
+    }
+    n += sum;
+    if (e <= g.E) start[e] = v, units[e] = n;
+    most = last = __shfl(v, 63);
+    sum = __shfl(n, 63);
+  }
+}
+
+// The group that unit u lies in: as many groups end at or before it.
+__device__ __forceinline__ int group_of(const int* units, int E, int u, int lane) {
+  int e = 0;
+  for (int base = 0; base < E; base += 64) {
+    const bool past = base + lane < E && units[min(base + lane + 1, E)] <= u;
+    e += __builtin_popcountll(__builtin_amdgcn_ballot_w64(past));
+  }
+  return e;
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Row r of those that belong to no group (in front of the first and behind the last), of `rest` in all.
+__device__ __forceinline__ int row_outside(int r, int first, int end) { return r < first ? r : end + r - first; }
+
+// ------------------------------------------------------------------------------------------------ host side
+
+static inline int check_groups(const fp4_groups* g) {
+  if (!g || !g->offsets) return FP4_ERR_ARG;
+  if (g->bits != 32 && g->bits != 64) return FP4_ERR_ARG;
+  if (g->count < 1) return FP4_ERR_SHAPE;
+  if (g->count > MAX_GROUPS) return FP4_ERR_UNSUPPORTED;
+  return fp4_aligned(g->offsets, (uintptr_t)g->bits / 8) ? FP4_OK : FP4_ERR_ALIGN;
+}
+
+static inline Groups groups_of(const fp4_groups& g) { return {g.offsets, (int)g.count, g.bits == 64, 0}; }
+
+// The most tiles of `rows` rows that T rows in E groups can make.
+static inline int64_t most_tiles(int64_t T, int64_t E, int64_t rows) {
+  const int64_t some = E < T ? E : T;
+  return (T - some) / rows + some;
+}
+
+int launch_rows_grouped(int x_type, int out_type, int T, int N, int K, const Groups& groups, const void* x, int64_t ldx, const fp4_mx* a,
+                        const fp4_mx& b, int64_t step_q, int64_t step_s, const fp4_epilogue* epi, void* y, int64_t ldy, int fill,
+                        hipStream_t st);
+
+}  // namespace mx

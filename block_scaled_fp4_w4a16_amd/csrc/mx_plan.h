@@ -86,4 +86,32 @@ inline bool fused(int64_t M, int64_t N, int64_t K) {
   return M <= 16 && (N + 15) / 16 * stages_of(K) * (M + 3) <= 32768;
 }
 
+// The tiles of a product of T rows in E groups, whose sizes only the device knows, with N columns and depth K: the cheapest
+// by the figures above for groups of equal size, each of which ends inside a tile. 0: rows_grouped_kernel, for up to 16 rows.
+inline int grouped_tile(int64_t T, int64_t N, int64_t K, int64_t E, int cus) {
+  if (T <= 16) return 0;
+  const double some = E < T ? E : T, each = T / some, least = 3.5 + some * N * K * (17 / 32.) / 5e6;
+  int tile = 0;
+  double best = 1e30;
+  for (const TileCost& c : TILE_COSTS) {
+    const double down = each / c.tile + 0.5, rows = some * (down > 1 ? down : 1);
+    double us = tiles_us(c, (int64_t)(rows * ((N + c.tile - 1) / c.tile)), (stages_of(K) + 1) & ~1, cus);
+    if (us < least) us = least;
+    if (us < best) best = us, tile = c.tile;
+  }
+  return tile;
+}
+
+// The tiles of E products of M x N outputs that contract T rows between them.
+inline int gradient_tile(int64_t T, int64_t M, int64_t N, int64_t E, int cus) {
+  int tile = 0;
+  double best = 1e30;
+  for (const TileCost& c : TILE_COSTS) {
+    const int64_t tiles = E * ((M + c.tile - 1) / c.tile) * ((N + c.tile - 1) / c.tile);
+    const double us = tiles_us(c, tiles, (stages_of((T + E - 1) / E) + 1) & ~1, cus);
+    if (us < best) best = us, tile = c.tile;
+  }
+  return tile;
+}
+
 }  // namespace mx

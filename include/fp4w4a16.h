@@ -387,6 +387,121 @@ int w4a4_linear(int x_type, int out_type, int64_t M, int64_t N, int64_t K, const
 /* Workspace bytes of w4a4_linear for this shape on the current device (0: it takes none), or a negative status. */
 int64_t w4a4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
+/*
+ * MXFP4 products with an epilogue, in the product's own kernels:
+ *
+ *     z = A B^T + bias          (FP32; bias[N], added to every row)
+ *     y = f(z) + residual       (rounded once, to y's type; residual[M][N])
+ *
+ * f: none, relu, silu (z / (1 + exp(-z))), gelu (z times the normal distribution function) or gelu by tanh
+ * (z / (1 + exp(-2 sqrt(2 / pi) (z + 0.044715 z^3)))). f of an infinity is what these formulas give in FP32: infinity or,
+ * for minus infinity and an f other than relu, NaN.
+ * Bias and residual are FP32, bf16 or FP16, each with the alignment of its type; NULL leaves one out. The residual may be y
+ * itself (the same address, row stride and type), which then is added to; any other overlap of y, z and the inputs is not
+ * allowed. z, if not NULL, receives z in FP32 with a row stride of ldz elements: what a backward pass takes f' at.
+ */
+enum {
+  FP4_ACT_NONE = 0,
+  FP4_ACT_RELU = 1,
+  FP4_ACT_SILU = 2,
+  FP4_ACT_GELU = 3,
+  FP4_ACT_GELU_TANH = 4
+};
+
+typedef struct fp4_epilogue {
+  const void* bias;
+  const void* residual;
+  float* z;
+  int64_t ldr;        /* elements from one row of the residual to the next */
+  int64_t ldz;
+  int bias_type;      /* FP4_TYPE_*; not looked at where the pointer is NULL */
+  int residual_type;
+  int activation;     /* FP4_ACT_* */
+} fp4_epilogue;
+
+/*
+ * w4a4_matmul and w4a4_linear with an epilogue: the same operands, kernels and workspaces (w4a4_matmul_workspace_bytes(),
+ * w4a4_linear_workspace_bytes()). Errors as theirs, and for the epilogue FP4_ERR_ARG (NULL, unknown activation or type),
+ * FP4_ERR_SHAPE (a stride below N), FP4_ERR_ALIGN, FP4_ERR_UNSUPPORTED (a stride too large).
+ */
+int w4a4_matmul_epilogue(int out_type, int64_t M, int64_t N, int64_t K, const fp4_mx* a, const fp4_mx* b,
+                         const fp4_epilogue* epilogue, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                         void* stream);
+int w4a4_linear_epilogue(int x_type, int out_type, int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx,
+                         const fp4_mx* b, const fp4_epilogue* epilogue, void* y, int64_t ldy, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * Rows in groups, one group per expert: group e's rows are [offsets[e], offsets[e + 1]), e = 0 .. count - 1. The count + 1
+ * bounds lie in DEVICE memory and are read by the kernels, so no size of a group is known to the host. Bounds are meant to
+ * grow from 0 or more to at most the number of rows T; whatever they hold, nothing outside the operands is touched: a bound
+ * counts as no less than those in front of it, 0 at least and T at most. Groups may be empty. count is 1 .. 512.
+ */
+typedef struct fp4_groups {
+  const void* offsets;  /* count + 1 bounds (device) */
+  int64_t count;
+  int bits;             /* 32 or 64: int32_t or int64_t bounds */
+} fp4_groups;
+
+/*
+ * The products of a mixture of experts: row t of group e takes the N weight rows of expert e,
+ *
+ *     y[t][n] = f(sum_k A[t][k] B[e N + n][k] + bias[e N + n]) + residual[t][n]
+ *
+ * with A of T rows, B of count N rows (experts one after the other) and a bias of count N values. epilogue may be NULL.
+ * Rows of y that belong to no group (in front of the first bound, behind the last) are left as they are, or, where `fill` is
+ * not 0, become the residual, or zeros without one; z's are left as they are.
+ * w4a4_grouped_linear takes dense x[T][K], quantised along its rows in the call as w4a4_linear does, and at least
+ * w4a4_grouped_linear_workspace_bytes() of workspace (0: none is taken). T = 0 is a no-op. Deterministic.
+ * Errors: those of w4a4_matmul_epilogue and w4a4_linear_epilogue; for the groups FP4_ERR_ARG (NULL, `bits`), FP4_ERR_SHAPE (no
+ * group), FP4_ERR_UNSUPPORTED (over 512 groups; count N over 2^30), FP4_ERR_ALIGN.
+ */
+int w4a4_grouped_matmul(int out_type, int64_t T, int64_t N, int64_t K, const fp4_groups* groups, const fp4_mx* a,
+                        const fp4_mx* b, const fp4_epilogue* epilogue, int fill, void* y, int64_t ldy, void* stream);
+int w4a4_grouped_linear(int x_type, int out_type, int64_t T, int64_t N, int64_t K, const fp4_groups* groups, const void* x,
+                        int64_t ldx, const fp4_mx* b, const fp4_epilogue* epilogue, int fill, void* y, int64_t ldy,
+                        void* workspace, size_t workspace_bytes, void* stream);
+int64_t w4a4_grouped_linear_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t count);
+
+/*
+ * What the backward passes of these products are made of.
+ *
+ * fp4_quantize_mxfp4_grouped: x[T][K] -> MXFP4 along its rows (`rows`: T rows of depth K) and / or along its columns
+ * (`cols`: K rows, whose depth holds the groups one after the other, each from a position that is a multiple of 256 on and
+ * padded with zeros to the next one: fp4_grouped_depth(T, count) positions in all, those behind the last group's untouched).
+ * Blocks along the columns so begin anew at each group's first row. `groups` may have offsets = NULL: T / count rows each
+ * (T a multiple of count). Rows of no group are not in `cols`; in `rows` they are left as they are.
+ * With `gradient`, D = x f'(z), rounded to x's type, is quantised in x's place (z NULL: D = x), and dbias[count][K], if not
+ * NULL, receives the sum of x f'(z) over each group's rows (held in FP32, its tiles' sums added in FP64, rounded once):
+ * then at least fp4_grouped_sums_bytes() of workspace, 16-byte aligned, is needed.
+ * rows and cols may both be NULL if dbias is not. Deterministic. T = 0: dbias becomes zeros.
+ *
+ * w4a4_grouped_gradient: the weights' gradients, dw[count][N][K] with rows ldw apart, dw_e[n][k] = sum over group e's rows t of
+ * A[n][t] B[k][t], from two operands along the columns made as above (A of N rows from the gradient, B of K rows from x, both
+ * of fp4_grouped_depth(T, count) positions). A group without rows gets zeros.
+ *
+ * w4a4_grouped_matmul_t: y[t][k] = sum_n A[t][n] B_e[k][n], A of T rows and depth N, B the weights [count][N][K] along their
+ * columns: one operand of K rows made by fp4_quantize_mxfp4_grouped with groups of N rows each. Rows of no group as in
+ * w4a4_grouped_matmul. Errors of all three as above; a NULL y or dw is FP4_ERR_ARG.
+ */
+typedef struct fp4_gradient {
+  const float* z;     /* FP32 [T][K], or NULL */
+  void* dbias;        /* [count][K], or NULL */
+  int64_t ldz;
+  int activation;     /* FP4_ACT_* of z */
+  int dbias_type;     /* FP4_TYPE_* */
+} fp4_gradient;
+
+int64_t fp4_grouped_depth(int64_t T, int64_t count);
+int64_t fp4_grouped_sums_bytes(int64_t T, int64_t K, int64_t count);
+int fp4_quantize_mxfp4_grouped(int type, int64_t T, int64_t K, const void* x, int64_t ldx, const fp4_groups* groups,
+                               const fp4_mx* rows, const fp4_mx* cols, const fp4_gradient* gradient, void* workspace,
+                               size_t workspace_bytes, void* stream);
+int w4a4_grouped_gradient(int out_type, int64_t T, int64_t N, int64_t K, const fp4_groups* groups, const fp4_mx* a,
+                          const fp4_mx* b, void* dw, int64_t ldw, void* stream);
+int w4a4_grouped_matmul_t(int out_type, int64_t T, int64_t N, int64_t K, const fp4_groups* groups, const fp4_mx* a,
+                          const fp4_mx* b, int fill, void* y, int64_t ldy, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
