@@ -98,6 +98,13 @@ __device__ __forceinline__ uint32_t to16(int type, float v) {
   return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v);
 }
 
+// Two FP32 sums -> two outputs of a 16-bit type in one register, rounded to nearest even.
+template <int OUT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (OUT == FP4_TYPE_BF16) return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+  else return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+}
+
 // Four consecutive outputs y[0 .. n - 1], n <= 4, of the given type; one vector store where all four exist and
 // the address allows it.
 __device__ __forceinline__ void store4(int type, void* y, int64_t at, const f32x4& v, int n, bool vec) {

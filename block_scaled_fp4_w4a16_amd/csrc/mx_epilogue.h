@@ -11,47 +11,49 @@ constexpr float TANH_1 = 1.59576912f, TANH_3 = 0.0713548163f;  // 2 sqrt(2 / pi)
 // 1 / (1 + 2^u), and its limits 0 and 1 at infinities.
 __device__ __forceinline__ float sigmoid2(float u) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u)); }
 
-// The logistic function that silu (z s(z)) and gelu by tanh (z s(2 sqrt(2 / pi) (z + 0.044715 z^3))) are made of. z^2 is held
-// below what makes s 0 or 1 anyway, so that no 0 times infinity arises.
-__device__ __forceinline__ float logistic(int act, float z) {
-  const float k1 = act == FP4_ACT_SILU ? -LOG2E : -LOG2E * TANH_1, k3 = act == FP4_ACT_SILU ? 0.0f : -LOG2E * TANH_3;
-  return sigmoid2(z * (k1 + k3 * fminf(z * z, 1e4f)));
-}
+// What z is multiplied by in silu, and in gelu by tanh: s(2 sqrt(2 / pi) (z + 0.044715 z^3)), where z^2 is held below what makes
+// s 0 or 1 anyway, so that no infinity less infinity arises.
+__device__ __forceinline__ float silu_factor(float z) { return sigmoid2(z * -LOG2E); }
+__device__ __forceinline__ float tanh_factor(float z) { return sigmoid2(z * (-LOG2E * TANH_1 - LOG2E * TANH_3 * fminf(z * z, 1e4f))); }
 
-// The normal distribution function at z, and exp(-z^2 / 2) for its density. With a = |z| / sqrt 2 and t = 1 / (1 + 0.33 a),
-// erfc(a) = t P(t) exp(-a^2), P a polynomial fitted to erfc(a) exp(a^2) / t for a up to 10.5 with relative weights: 1.1e-7
-// off at most, so the distribution has its relative accuracy in the lower tail as well.
-__device__ __forceinline__ float normal(float z, float& e) {
+// The normal distribution's upper tail at |z|, and e = exp(-z^2 / 2) for its density. With a = |z| / sqrt 2 and
+// t = 1 / (1 + 0.33 a), erfc(a) = t P(t) exp(-a^2), P a polynomial fitted to erfc(a) exp(a^2) / t for a up to 10.5 with relative
+// weights: 1.1e-7 off at most, so that the tail has its relative accuracy. At infinities both are 0.
+__device__ __forceinline__ float normal_tail(float z, float& e) {
   const float t = __builtin_amdgcn_rcpf(1.0f + (0.33f * 0.707106781f) * fabsf(z));
-  float p = -0.134472281f;
-  p = p * t + 0.456568509f;
-  p = p * t - 0.344742447f;
-  p = p * t + 0.402482688f;
-  p = p * t + 0.0504948199f;
-  p = p * t + 0.200193852f;
-  p = p * t + 0.183129117f;
-  p = p * t + 0.186345816f;
+  float p = -0.5f * 0.134472281f;
+  p = p * t + 0.5f * 0.456568509f;
+  p = p * t - 0.5f * 0.344742447f;
+  p = p * t + 0.5f * 0.402482688f;
+  p = p * t + 0.5f * 0.0504948199f;
+  p = p * t + 0.5f * 0.200193852f;
+  p = p * t + 0.5f * 0.183129117f;
+  p = p * t + 0.5f * 0.186345816f;
   e = __builtin_amdgcn_exp2f(z * z * (-0.5f * LOG2E));
-  const float half = 0.5f * p * t * e;
-  return z < 0 ? half : 1.0f - half;
+  return p * t * e;
 }
 
-// f(z) of W values in place; `act` is the same for the whole wave.
+// f(z) of W values in place; `act` is the same for the whole wave. A NaN stays; f(infinity) is infinity; f(-infinity) is 0 for
+// relu and gelu and NaN for silu and gelu by tanh (minus infinity times 0).
 template <int W>
 __device__ __forceinline__ void activate(int act, float (&z)[W]) {
   if (act == FP4_ACT_NONE) return;
   if (act == FP4_ACT_RELU) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) z[i] = z[i] < 0 ? 0.0f : z[i];  // a NaN stays
+    for (int i = 0; i < W; ++i) z[i] = z[i] < 0 ? 0.0f : z[i];
   } else if (act == FP4_ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
+    for (int i = 0; i < W; ++i) {  // max(z, 0) - |z| tail: the maximum drops a NaN, the tail brings it back
       float e;
-      z[i] *= normal(z[i], e);
+      const float tail = normal_tail(z[i], e);
+      z[i] = fmaf(-fminf(fabsf(z[i]), 1e30f), tail, fmaxf(z[i], 0.0f));
     }
+  } else if (act == FP4_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) z[i] *= silu_factor(z[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < W; ++i) z[i] *= logistic(act, z[i]);
+    for (int i = 0; i < W; ++i) z[i] *= tanh_factor(z[i]);
   }
 }
 
@@ -60,16 +62,16 @@ __device__ __forceinline__ float slope(int act, float z) {
   if (act == FP4_ACT_RELU) return z > 0 ? 1.0f : z <= 0 ? 0.0f : z;
   z = z > 128.0f ? 128.0f : z < -128.0f ? -128.0f : z;
   if (act == FP4_ACT_SILU) {
-    const float s = logistic(act, z);
+    const float s = silu_factor(z);
     return s + z * s * (1.0f - s);
   }
   if (act == FP4_ACT_GELU) {
     float e;
-    const float p = normal(z, e);
-    return p + z * e * 0.398942280f;
+    const float tail = normal_tail(z, e);
+    return (z < 0 ? tail : 1.0f - tail) + z * e * 0.398942280f;
   }
   if (act == FP4_ACT_GELU_TANH) {
-    const float s = logistic(act, z);
+    const float s = tanh_factor(z);
     return s + z * s * (1.0f - s) * (TANH_1 + 3.0f * TANH_3 * z * z);
   }
   return 1.0f;

@@ -3,7 +3,7 @@
 //
 // The sums leave through LDS as FP32 (y's rounding comes behind the residual), 16 rows of a wave's columns at a time: a lane then
 // holds 8 neighbouring columns of a row (4 of FP32), so that residual, z and y move in whole lines, and bias and activation
-// are taken in between. The residual's values are asked for two parts before they are added.
+// are taken in between.
 #pragma once
 #include "mx_epilogue.h"
 #include "mx_groups.h"
@@ -23,6 +23,7 @@ struct Args {
   int64_t ldy;
   int M, N, K;            // DEPTH: K rows in groups
   int tiles_m, tiles_n;   // ROWS: tiles_m is not known
+  int whole;              // rows of y, z and the residual suit store_whole
   int fill;               // ROWS: rows of no group become the residual, or zero
   fp4_epilogue epi;
   Groups groups;
@@ -44,96 +45,233 @@ __device__ __forceinline__ void walk(int t, int tiles_m, int tiles_n, int& tm, i
   tm = band * BAND + in - tn * h;
 }
 
-// Sums S of a wave, 16 rows and the columns of a half, to its LDS.
-template <int S, class G, int SPLIT>
-__device__ __forceinline__ void stage_sums(const f32x4 (&acc)[G::TM][G::TN], uint8_t* in) {
-  constexpr int TJ = G::TN / SPLIT;
-#pragma unroll
-  for (int j = 0; j < TJ; ++j) {
-    f32x4 v = acc[S / SPLIT][S % SPLIT * TJ + j];
-    asm volatile("; part %1" : "+a"(v) : "n"(S));  // nothing to do, but different in each part (stage_any)
-    *reinterpret_cast<f32x4*>(in + j * 64) = v;
-  }
+__device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)p;
 }
-// The same for s in [FROM, TO): registers have no index, so a branch finds them. Branches alike would be made one again, with
-// the sums in memory.
-template <int FROM, int TO, class G, int SPLIT>
-__device__ __forceinline__ void stage_any(int s, const f32x4 (&acc)[G::TM][G::TN], uint8_t* in) {
-  if constexpr (TO - FROM == 1) {
+
+// LDS accesses of the way out are written out: with LDS that direct loads write to, the compiler has every read and write of
+// LDS wait for all of a wave's memory accesses, stores included, a thousand cycles each. A wave's LDS accesses stay in order.
+// Part S of a wave's sums, 16 rows and the columns of a half, to its LDS. (The part's number in the text keeps the branches
+// of stage_any apart: branches alike would be made one again, with the sums in memory.)
+template <int S, class G, int SPLIT>
+__device__ __forceinline__ void stage_sums(const f32x4 (&acc)[G::TM][G::TN], uint32_t in) {
+  constexpr int I = S / SPLIT, J = S % SPLIT * (G::TN / SPLIT);
+  if constexpr (G::TN / SPLIT == 4)
+    asm volatile("ds_write_b128 %0, %1\n\tds_write_b128 %0, %2 offset:64\n\tds_write_b128 %0, %3 offset:128\n\t"
+                 "ds_write_b128 %0, %4 offset:192 ; part %5"
+                 :
+                 : "v"(in), "a"(acc[I][J]), "a"(acc[I][J + 1]), "a"(acc[I][J + 2]), "a"(acc[I][J + 3]), "n"(S)
+                 : "memory");
+  else
+    asm volatile("ds_write_b128 %0, %1\n\tds_write_b128 %0, %2 offset:64 ; part %3"
+                 :
+                 : "v"(in), "a"(acc[I][J]), "a"(acc[I][J + 1]), "n"(S)
+                 : "memory");
+}
+// The same for s = FROM, FROM + BY, .. < TO: registers have no index, so branches find them.
+template <int FROM, int TO, int BY, class G, int SPLIT>
+__device__ __forceinline__ void stage_any(int s, const f32x4 (&acc)[G::TM][G::TN], uint32_t in) {
+  if constexpr (TO - FROM <= BY) {
     stage_sums<FROM, G, SPLIT>(acc, in);
   } else {
-    constexpr int MID = (FROM + TO) / 2;
-    if (s < MID) stage_any<FROM, MID, G, SPLIT>(s, acc, in);
-    else stage_any<MID, TO, G, SPLIT>(s, acc, in);
+    constexpr int MID = FROM + (TO - FROM) / BY / 2 * BY;
+    if (s < MID) stage_any<FROM, MID, BY, G, SPLIT>(s, acc, in);
+    else stage_any<MID, TO, BY, G, SPLIT>(s, acc, in);
+  }
+}
+// A lane's share of a part back from LDS: 16 bytes at each of two (N 2) or four places.
+template <int N, int O1, int O2, int O3>
+__device__ __forceinline__ void read_part(uint32_t out, f32x4 (&v)[N]) {
+  static_assert(N == 2 || N == 4, "");
+  if constexpr (N == 4)
+    asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:%5\n\tds_read_b128 %2, %4 offset:%6\n\t"
+                 "ds_read_b128 %3, %4 offset:%7\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+                 : "v"(out), "n"(O1), "n"(O2), "n"(O3)
+                 : "memory");
+  else
+    asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %2 offset:%3\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(v[0]), "=&v"(v[1])
+                 : "v"(out), "n"(O1)
+                 : "memory");
+}
+
+// How a wave's sums leave: in parts of 16 rows and COLS columns.
+template <int OUT, class G>
+struct Way {
+  static constexpr int SPLIT = G::TN == 8 ? 2 : 1, COLS = 16 * G::TN / SPLIT, STRIDE = COLS * 4 + 16, ALL = G::TM * SPLIT;
+  static constexpr int W = OUT == FP4_TYPE_F32 ? 4 : 8;                     // columns of a lane
+  static constexpr int PER = COLS / W, ROWS = 64 / PER, STEPS = 16 / ROWS;  // lanes per row, rows per step
+  static constexpr int READS = STEPS * W / 4;                               // of 16 bytes, per lane and part
+  static constexpr int offset(int r) { return r / (W / 4) * ROWS * STRIDE + r % (W / 4) * 16; }
+  static __device__ __forceinline__ void read(uint32_t out, f32x4 (&v)[READS]) {
+    read_part<READS, offset(1), offset(2), offset(3)>(out, v);
+  }
+};
+
+// W values of a 16-bit type (32-bit, if F32) by a buffer access, whose descriptor drops what lies behind its last row.
+template <bool F32, int W>
+__device__ __forceinline__ Raw<W> buffer_raw(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+  Raw<W> v{};
+  if constexpr (F32) {
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) {
+      const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(r, at + 16 * i, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v.v[4 * i + j] = x[j];
+    }
+  } else if constexpr (W == 8) {
+    const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v.v[j] = x[j];
+  } else {
+    const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0);
+    v.v[0] = x[0], v.v[1] = x[1];
+  }
+  return v;
+}
+template <int OUT, int W>
+__device__ __forceinline__ void buffer_store(__amdgpu_buffer_rsrc_t r, uint32_t at, const float (&f)[W]) {
+  if constexpr (OUT == FP4_TYPE_F32) {
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) {
+      u32x4 x;
+      __builtin_memcpy(&x, f + 4 * i, 16);
+      __builtin_amdgcn_raw_buffer_store_b128(x, r, at + 16 * i, 0, 0);
+    }
+  } else {
+    static_assert(W == 8, "");
+    __builtin_amdgcn_raw_buffer_store_b128(
+        u32x4{pack2<OUT>(f[0], f[1]), pack2<OUT>(f[2], f[3]), pack2<OUT>(f[4], f[5]), pack2<OUT>(f[6], f[7])}, r, at, 0, 0);
+  }
+}
+
+// This wave's sums to y where all their columns exist, rows are aligned to 4 bytes and not too far apart for a descriptor.
+// RES: 0 no residual, 1 of 16 bits, 2 of 32; Z: z is kept. Nothing branches around a memory access, so the compiler knows how
+// many a residual has behind it: it is asked for U parts ahead and waits for no store that is younger.
+template <int OUT, class G, int RES, bool Z>
+__device__ __forceinline__ void store_whole(const f32x4 (&acc)[G::TM][G::TN], const fp4_epilogue& epi, int64_t bias_at, void* y,
+                                            int64_t ldy, int row0, int rows, int col0, int lane, uint8_t* stage) {
+  using P = Way<OUT, G>;
+  constexpr int W = P::W, U = P::ALL < 4 ? P::ALL : 4, EB = elem_bytes(OUT), RB = RES == 2 ? 4 : 2, WIDTH = P::COLS * P::SPLIT;
+  const int n = lane & 15, g = lane >> 4, r = lane / P::PER, c = lane % P::PER * W;
+  const uint32_t in = lds_address(stage) + n * P::STRIDE + 16 * g, out = lds_address(stage) + r * P::STRIDE + 4 * c;
+  const auto descriptor = [&](const void* p, int64_t ld, int eb) {
+    return fp4::make_rsrc(static_cast<const uint8_t*>(p) + (row0 * ld + col0) * eb, (uint32_t)(((rows - 1) * (int)ld + WIDTH) * eb));
+  };
+  const auto place = [&](int s, int k, int64_t ld, int eb) {
+    return (uint32_t)(((16 * (s / P::SPLIT) + k * P::ROWS + r) * (int)ld + s % P::SPLIT * P::COLS + c) * eb);
+  };
+  const auto to = descriptor(y, ldy, EB);
+  auto from = to, keep = to;
+  if constexpr (RES != 0) from = descriptor(epi.residual, epi.ldr, RB);
+  if constexpr (Z) keep = descriptor(epi.z, epi.ldz, 4);
+  const int res_type = RES == 2 ? FP4_TYPE_F32 : epi.residual_type == FP4_TYPE_BF16 ? FP4_TYPE_BF16 : FP4_TYPE_F16;
+
+  float bias[P::SPLIT][W];
+#pragma unroll
+  for (int h = 0; h < P::SPLIT; ++h) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) bias[h][i] = 0;
+    if (epi.bias) values_of(epi.bias_type, load_raw<W>(epi.bias_type, epi.bias, bias_at + col0 + h * P::COLS + c, W), bias[h]);
+  }
+  Raw<W> ahead[U][P::STEPS];
+  if constexpr (RES != 0)
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < P::STEPS; ++k) ahead[u][k] = buffer_raw<RES == 2, W>(from, place(u, k, epi.ldr, RB));
+  const int all = min(P::ALL, (rows + 15) / 16 * P::SPLIT);
+#pragma unroll 1
+  for (int s0 = 0; s0 < all; s0 += U) {  // parts without rows in the last round: their stores are dropped
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int s = s0 + u;
+      if (u == 0) stage_any<0, P::ALL, U, G, P::SPLIT>(s, acc, in);
+      else if (u == 1) stage_any<1, P::ALL + 1, U, G, P::SPLIT>(s, acc, in);
+      else if (u == 2) stage_any<2, P::ALL + 2, U, G, P::SPLIT>(s, acc, in);
+      else stage_any<3, P::ALL + 3, U, G, P::SPLIT>(s, acc, in);
+      f32x4 v[P::READS];
+      P::read(out, v);
+#pragma unroll
+      for (int k = 0; k < P::STEPS; ++k) {
+        float f[W];
+        __builtin_memcpy(f, v + k * (W / 4), 4 * W);
+#pragma unroll
+        for (int i = 0; i < W; ++i) f[i] += bias[u % P::SPLIT][i];
+        if constexpr (Z) buffer_store<FP4_TYPE_F32>(keep, place(s, k, epi.ldz, 4), f);
+        activate(epi.activation, f);
+        if constexpr (RES != 0) {
+          float add[W];
+          values_of(res_type, ahead[u][k], add);
+#pragma unroll
+          for (int i = 0; i < W; ++i) f[i] += add[i];
+          ahead[u][k] = buffer_raw<RES == 2, W>(from, place(s + U, k, epi.ldr, RB));  // past the tile: nothing
+        }
+        buffer_store<OUT>(to, place(s, k, ldy, EB), f);
+      }
+    }
+  }
+}
+
+// The same where columns end inside the tile, or rows lie at any alignment: accesses of what is there.
+template <int OUT, class G>
+__device__ __forceinline__ void store_part(const f32x4 (&acc)[G::TM][G::TN], const fp4_epilogue& epi, int64_t bias_at, void* y,
+                                           int64_t ldy, int row0, int rows, int col0, int N, int lane, uint8_t* stage) {
+  using P = Way<OUT, G>;
+  constexpr int W = P::W;
+  const int n = lane & 15, g = lane >> 4, r = lane / P::PER;
+  const uint32_t in = lds_address(stage) + n * P::STRIDE + 16 * g, out = lds_address(stage) + r * P::STRIDE + lane % P::PER * (4 * W);
+  const int all = min(P::ALL, (rows + 15) / 16 * P::SPLIT);
+#pragma unroll 1
+  for (int s = 0; s < all; ++s) {
+    stage_any<0, P::ALL, 1, G, P::SPLIT>(s, acc, in);
+    f32x4 v[P::READS];
+    P::read(out, v);
+    const int col = col0 + s % P::SPLIT * P::COLS + lane % P::PER * W, left = N - col;
+    float bias[W] = {};
+    if (epi.bias && left > 0) values_of(epi.bias_type, load_raw<W>(epi.bias_type, epi.bias, bias_at + col, left), bias);
+#pragma unroll
+    for (int k = 0; k < P::STEPS; ++k) {
+      const int in_rows = 16 * (s / P::SPLIT) + k * P::ROWS + r;
+      const int64_t row = row0 + in_rows;
+      const bool there = in_rows < rows && left > 0;
+      float f[W], add[W] = {};
+      __builtin_memcpy(f, v + k * (W / 4), 4 * W);
+      if (epi.residual && there) values_of(epi.residual_type, load_raw<W>(epi.residual_type, epi.residual, row * epi.ldr + col, left), add);
+#pragma unroll
+      for (int i = 0; i < W; ++i) f[i] += bias[i];
+      if (epi.z && there) store_values<FP4_TYPE_F32>(epi.z, row * epi.ldz + col, f, left);
+      activate(epi.activation, f);
+      if (epi.residual)
+#pragma unroll
+        for (int i = 0; i < W; ++i) f[i] += add[i];
+      if (there) store_values<OUT>(y, row * ldy + col, f, left);
+    }
   }
 }
 
 // This wave's sums, rows row0 + 16 i .., columns col0 + 16 j .., to y; rows from `end` on and columns from N on are not there.
-// One loop body serves every 16 rows: written out, 256 sums' way through it would be 130 KB of code.
+// `whole`: rows of y, z and the residual suit store_whole.
 template <int OUT, class G>
 __device__ __forceinline__ void store_epilogue(const f32x4 (&acc)[G::TM][G::TN], const fp4_epilogue& epi, int64_t bias_at, void* y,
-                                               int64_t ldy, int row0, int end, int col0, int N, int lane, uint8_t* stage) {
-  constexpr int SPLIT = G::TN == 8 ? 2 : 1, COLS = 16 * G::TN / SPLIT, STRIDE = COLS * 4 + 16, ALL = G::TM * SPLIT;
-  constexpr int W = OUT == FP4_TYPE_F32 ? 4 : 8;                   // columns of a lane
-  constexpr int PER = COLS / W, ROWS = 64 / PER, STEPS = 16 / ROWS;  // lanes per row, rows per step
-  const int n = lane & 15, g = lane >> 4;
-  uint8_t* const in = stage + n * STRIDE + 16 * g;
-  const uint8_t* const out = stage + lane / PER * STRIDE + lane % PER * (4 * W);
-  const int row_of = row0 + lane / PER, col_of = col0 + lane % PER * W;
-  const int all = min(ALL, (end - row0 + 15) / 16 * SPLIT);
-  if (all <= 0 || col0 >= N) return;
-
-  float bias[SPLIT][W];
-#pragma unroll
-  for (int h = 0; h < SPLIT; ++h) {
-#pragma unroll
-    for (int i = 0; i < W; ++i) bias[h][i] = 0;
-    const int c = col_of + h * COLS;
-    if (epi.bias && c < N) values_of(epi.bias_type, load_raw<W>(epi.bias_type, epi.bias, bias_at + c, N - c), bias[h]);
+                                               int64_t ldy, int row0, int end, int col0, int N, int lane, uint8_t* stage, int whole) {
+  const int rows = min(end - row0, 16 * G::TM);
+  if (rows <= 0 || col0 >= N) return;
+#define MX_WHOLE(RES, Z) store_whole<OUT, G, RES, Z>(acc, epi, bias_at, y, ldy, row0, rows, col0, lane, stage)
+  if (!whole || col0 + 16 * G::TN > N) {
+    store_part<OUT, G>(acc, epi, bias_at, y, ldy, row0, rows, col0, N, lane, stage);
+  } else if (!epi.residual) {
+    if (epi.z) MX_WHOLE(0, true);
+    else MX_WHOLE(0, false);
+  } else if (epi.residual_type == FP4_TYPE_F32) {
+    if (epi.z) MX_WHOLE(2, true);
+    else MX_WHOLE(2, false);
+  } else {
+    if (epi.z) MX_WHOLE(1, true);
+    else MX_WHOLE(1, false);
   }
-  // part s: row tile s / SPLIT, columns' half s % SPLIT
-  Raw<W> ahead[2][STEPS] = {};
-  const auto ask = [&](int s, Raw<W>(&r)[STEPS]) {
-    const int row = row_of + 16 * (s / SPLIT), col = col_of + s % SPLIT * COLS;
-#pragma unroll
-    for (int k = 0; k < STEPS; ++k)
-      if (row + k * ROWS < end && col < N)
-        r[k] = load_raw<W>(epi.residual_type, epi.residual, (int64_t)(row + k * ROWS) * epi.ldr + col, N - col);
-  };
-  if (epi.residual) {
-    ask(0, ahead[0]);
-    if (all > 1) ask(1, ahead[1]);
-  }
-#pragma unroll 1
-  for (int s = 0; s < all; ++s) {
-    stage_any<0, ALL, G, SPLIT>(s, acc, in);
-    asm volatile("" ::: "memory");  // one wave's LDS accesses stay in order: no barrier
-    float add[STEPS][W];
-    if (epi.residual) {
-#pragma unroll
-      for (int k = 0; k < STEPS; ++k) {
-        values_of(epi.residual_type, ahead[0][k], add[k]);
-        ahead[0][k] = ahead[1][k];
-      }
-      if (s + 2 < all) ask(s + 2, ahead[1]);
-    }
-    const int row = row_of + 16 * (s / SPLIT), col = col_of + s % SPLIT * COLS, left = N - col;
-#pragma unroll
-    for (int k = 0; k < STEPS; ++k) {
-      float f[W];
-      __builtin_memcpy(f, out + k * ROWS * STRIDE, 4 * W);
-      const bool there = row + k * ROWS < end && col < N;
-#pragma unroll
-      for (int i = 0; i < W; ++i) f[i] += SPLIT == 2 && s % SPLIT ? bias[SPLIT - 1][i] : bias[0][i];
-      if (epi.z && there) store_values<FP4_TYPE_F32>(epi.z, (int64_t)(row + k * ROWS) * epi.ldz + col, f, left);
-      activate(epi.activation, f);
-      if (epi.residual)
-#pragma unroll
-        for (int i = 0; i < W; ++i) f[i] += add[k][i];
-      if (there) store_values<OUT>(y, (int64_t)(row + k * ROWS) * ldy + col, f, left);
-    }
-    asm volatile("" ::: "memory");
-  }
+#undef MX_WHOLE
 }
 
 // Rows of no group: the residual, or zero.
@@ -297,7 +435,7 @@ __global__ void __launch_bounds__(G::THREADS, G::LDS > 80 * 1024 ? G::WAVES / 4 
       stage = lds + w.wave * (16 * (64 * G::TN + 16));
     }
     void* const y = MODE == DEPTH ? static_cast<uint8_t*>(p.y) + (int64_t)job.e * p.M * p.ldy * elem_bytes(OUT) : p.y;
-    store_epilogue<OUT, G>(w.acc, p.epi, (int64_t)job.e * N, y, p.ldy, job.m0 + arow, job.end, job.n0 + brow - BM, N, w.lane, stage);
+    store_epilogue<OUT, G>(w.acc, p.epi, (int64_t)job.e * N, y, p.ldy, job.m0 + arow, job.end, job.n0 + brow - BM, N, w.lane, stage, p.whole);
     if (!STREAMED<G> || id >= total) break;
     job = next;
   }
@@ -305,9 +443,13 @@ __global__ void __launch_bounds__(G::THREADS, G::LDS > 80 * 1024 ? G::WAVES / 4 
   __builtin_amdgcn_s_waitcnt(0);
 }
 
+// A tensor whose rows store_whole can take: at most 2^31 bytes in 256 of them, each aligned to 4.
+static inline bool suits(const void* p, int64_t ld, int eb) { return !p || (fp4_aligned(p, 4) && ld * eb % 4 == 0 && ld * eb < (1 << 23)); }
+
 // `tiles`: the most tiles there can be.
 template <class G, int OUT, Mode MODE>
-static int launch_product(const Args& p, int64_t tiles, hipStream_t st) {
+static int launch_product(Args p, int64_t tiles, hipStream_t st) {
+  p.whole = suits(p.y, p.ldy, elem_bytes(OUT)) && suits(p.epi.residual, p.epi.ldr, elem_bytes(p.epi.residual_type)) && suits(p.epi.z, p.epi.ldz, 4);
   static Fp4LdsLimit limit;
   const int lds = G::LDS + (MODE == DENSE ? 0 : group_table_bytes(p.groups.E));
   limit.ensure(reinterpret_cast<const void*>(&product_kernel<G, OUT, MODE>), G::LDS + (MODE == DENSE ? 0 : group_table_bytes(MAX_GROUPS)));

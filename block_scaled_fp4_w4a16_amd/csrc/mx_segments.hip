@@ -19,12 +19,12 @@ struct Segments {
   float* sums;        // null: not wanted
   int64_t ldx, ldz;
   Groups groups;
-  int act, M, K, tiles_k, each_units;  // each_units: units per group where the groups are alike, else 0
+  int M, K, tiles_k, each_units;  // each_units: units per group where the groups are alike, else 0
 };
 
 // One row's four values of a lane -> x f'(z), the sums first, then rounded to x's type.
-template <int T, int R>
-__device__ __forceinline__ void gradient_row(uint32_t (&v)[R], const Raw<4>& z, int act, bool there, float (&sum)[4]) {
+template <int T, int ACT, int R>
+__device__ __forceinline__ void gradient_row(uint32_t (&v)[R], const u32x4& z, bool there, const bool (&in)[4], float (&sum)[4]) {
   float f[4];
   Raw<4> raw;
 #pragma unroll
@@ -32,17 +32,23 @@ __device__ __forceinline__ void gradient_row(uint32_t (&v)[R], const Raw<4>& z, 
   values_of(T, raw, f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[i] = there ? f[i] * slope(act, __builtin_bit_cast(float, z.v[i])) : 0.0f;
+    const uint32_t bits = z[i];  // (a bit cast of a vector's element itself takes the first one)
+    const float d = f[i] * slope(ACT, __builtin_bit_cast(float, bits));
+    f[i] = there && in[i] ? d : 0.0f;
     sum[i] += f[i];
+    asm volatile("" : "+v"(sum[i]));  // added here: where the sums are wanted or not, later, every value would have to be kept
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     if constexpr (T == FP4_TYPE_F32) v[i] = __builtin_bit_cast(uint32_t, f[i]);
-    else v[i] = to16(T, f[2 * i]) | to16(T, f[2 * i + 1]) << 16;
+    else v[i] = pack2<T>(f[2 * i], f[2 * i + 1]);
+    asm volatile("" : "+v"(v[i]));  // a pair stays one register: what is taken apart later would be kept apart from here on
   }
 }
 
-template <int T, int W, bool Z>
+// ACT: the activation whose derivative is taken, FP4_ACT_NONE where x is quantised as it is. (Told apart at each value, the four
+// would take 199 registers and a branch a value.)
+template <int T, int W, int ACT>
 __global__ void __launch_bounds__(64 * W) quantize_grouped_kernel(Segments p) {
   constexpr int EB = elem_bytes(T), R = Patch<T>::R, PARTS = UNIT / (32 * W);
   __shared__ u32x4 col_codes[256 * W];
@@ -100,20 +106,24 @@ __global__ void __launch_bounds__(64 * W) quantize_grouped_kernel(Segments p) {
     }
   }
   float sum[4] = {0, 0, 0, 0};
-  if constexpr (Z) {
-    const float* zr = p.z + (int64_t)from * p.ldz + col;
+  if constexpr (ACT != FP4_ACT_NONE) {
+    // four rows of z at a time, the next four on their way meanwhile: all 32 do not fit the registers. Rows behind the last
+    // one are not read; a lane at the matrix's edge reads into the next row, which `in` drops.
+    const auto zr = fp4::make_rsrc(p.z + (int64_t)from * p.ldz, (uint32_t)(min(last, 31) * (int)p.ldz + K) * 4);
+    const bool in[4] = {col < K, col + 1 < K, col + 2 < K, col + 3 < K};
+    u32x4 z[2][4];
+    const auto ask = [&](int b) {
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      __builtin_amdgcn_sched_barrier(0);  // eight rows of z at a time: all 32 do not fit the registers
-      Raw<4> z[8];
+      for (int i = 0; i < 4; ++i) z[b & 1][i] = __builtin_amdgcn_raw_buffer_load_b128(zr, ((4 * b + i) * (int)p.ldz + col) * 4, 0, 0);
+    };
+    ask(0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        z[i] = Raw<4>{};
-        if (col < K) z[i] = load_raw<4>(FP4_TYPE_F32, zr, 0, K - col);
-        if (8 * b + i < last) zr += p.ldz;
-      }
+    for (int b = 0; b < 8; ++b) {
+      if (b < 7) ask(b + 1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) gradient_row<T, R>(patch.v[8 * b + i], z[i], p.act, row0 + 8 * b + i < end, sum);
+      for (int i = 0; i < 4; ++i) gradient_row<T, ACT>(patch.v[4 * b + i], z[b & 1][i], row0 + 4 * b + i < end, in, sum);
+      __builtin_amdgcn_sched_barrier(0);
     }
   } else {
     if (row0 + 32 > end) {
@@ -269,7 +279,7 @@ extern "C" int fp4_quantize_mxfp4_grouped(int type, int64_t T, int64_t K, const 
     }
     if (z) {
       if (gradient->ldz < K) return FP4_ERR_SHAPE;
-      if (gradient->ldz > (1LL << 40)) return FP4_ERR_UNSUPPORTED;
+      if (gradient->ldz > (1LL << 23)) return FP4_ERR_UNSUPPORTED;  // 32 rows of it are addressed with 32 bits
       if (!fp4_aligned(gradient->z, 4)) return FP4_ERR_ALIGN;
     }
   }
@@ -301,18 +311,25 @@ extern "C" int fp4_quantize_mxfp4_grouped(int type, int64_t T, int64_t K, const 
     if (rows) p.rows = *rows;
     if (cols) p.cols = *cols;
     if (sums) p.sums = static_cast<float*>(workspace);
-    if (z) p.z = gradient->z, p.ldz = gradient->ldz, p.act = gradient->activation;
+    if (z) p.z = gradient->z, p.ldz = gradient->ldz;
     const dim3 grid((unsigned)(tk * units * parts)), block(64 * w);
+    const int act = z ? gradient->activation : FP4_ACT_NONE;
     int rc;
-#define MX_SEG(T_, W_) \
-  rc = z ? fp4_launch(quantize_grouped_kernel<T_, W_, true>, grid, block, 0, st, p) : fp4_launch(quantize_grouped_kernel<T_, W_, false>, grid, block, 0, st, p)
-#define MX_SEG_W(T_)      \
-  if (w == 8) MX_SEG(T_, 8); \
-  else MX_SEG(T_, 4)
-    if (type == FP4_TYPE_F32) { MX_SEG_W(FP4_TYPE_F32); }
-    else if (type == FP4_TYPE_BF16) { MX_SEG_W(FP4_TYPE_BF16); }
-    else { MX_SEG_W(FP4_TYPE_F16); }
+#define MX_SEG(T_, W_, ACT_) rc = fp4_launch(quantize_grouped_kernel<T_, W_, ACT_>, grid, block, 0, st, p)
+#define MX_SEG_ACT(T_, W_)                                              \
+  if (act == FP4_ACT_NONE) MX_SEG(T_, W_, FP4_ACT_NONE);                \
+  else if (act == FP4_ACT_RELU) MX_SEG(T_, W_, FP4_ACT_RELU);           \
+  else if (act == FP4_ACT_SILU) MX_SEG(T_, W_, FP4_ACT_SILU);           \
+  else if (act == FP4_ACT_GELU) MX_SEG(T_, W_, FP4_ACT_GELU);           \
+  else MX_SEG(T_, W_, FP4_ACT_GELU_TANH)
+#define MX_SEG_W(T_)                  \
+  if (w == 8) { MX_SEG_ACT(T_, 8); }  \
+  else { MX_SEG_ACT(T_, 4); }
+    if (type == FP4_TYPE_F32) { MX_SEG_W(FP4_TYPE_F32) }
+    else if (type == FP4_TYPE_BF16) { MX_SEG_W(FP4_TYPE_BF16) }
+    else { MX_SEG_W(FP4_TYPE_F16) }
 #undef MX_SEG_W
+#undef MX_SEG_ACT
 #undef MX_SEG
     if (rc) return rc;
   }

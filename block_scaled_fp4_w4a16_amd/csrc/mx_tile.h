@@ -241,13 +241,6 @@ struct Wave {
   }
 };
 
-// Two FP32 sums -> two outputs of a 16-bit type in one register, rounded to nearest even.
-template <int OUT>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (OUT == FP4_TYPE_BF16) return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
-  else return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
-}
-
 // ------------------------------------------------------------------------------------------------ host side
 
 struct LinearSpace {

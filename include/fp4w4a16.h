@@ -394,8 +394,8 @@ int64_t w4a4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *     y = f(z) + residual       (rounded once, to y's type; residual[M][N])
  *
  * f: none, relu, silu (z / (1 + exp(-z))), gelu (z times the normal distribution function) or gelu by tanh
- * (z / (1 + exp(-2 sqrt(2 / pi) (z + 0.044715 z^3)))). f of an infinity is what these formulas give in FP32: infinity or,
- * for minus infinity and an f other than relu, NaN.
+ * (z / (1 + exp(-2 sqrt(2 / pi) (z + 0.044715 z^3)))). f(infinity) is infinity; f(-infinity) is 0 for relu and gelu and, as the
+ * formulas give it in FP32, NaN for silu and gelu by tanh.
  * Bias and residual are FP32, bf16 or FP16, each with the alignment of its type; NULL leaves one out. The residual may be y
  * itself (the same address, row stride and type), which then is added to; any other overlap of y, z and the inputs is not
  * allowed. z, if not NULL, receives z in FP32 with a row stride of ldz elements: what a backward pass takes f' at.
