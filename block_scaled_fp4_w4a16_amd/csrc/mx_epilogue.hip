@@ -18,6 +18,11 @@ static void* ahead(const void* p, int64_t n, int type) {
   return p ? const_cast<uint8_t*>(static_cast<const uint8_t*>(p) + n * elem_bytes(type)) : nullptr;
 }
 
+static Plan plan_with(int64_t M, int64_t N, int64_t K, const fp4_epilogue& e, bool split = true) {
+  const bool erf = e.activation == FP4_ACT_GELU, other = !erf && e.activation > FP4_ACT_RELU;
+  return plan_of(M, N, K, fp4_device_cus(), split, epilogue_costs(erf, other, e.residual, e.z).of);
+}
+
 // `p`: the plan of the product. Columns that are a product of their own (p.first_n) have the epilogue's columns with them.
 static int run_epilogue(Plan p, int out_type, int64_t M, int64_t N, int64_t K, const fp4_mx& a, const fp4_mx& b, const fp4_epilogue& e,
                         void* y, int64_t ldy, void* ws, size_t ws_bytes, hipStream_t st) {
@@ -37,7 +42,7 @@ static int run_epilogue(Plan p, int out_type, int64_t M, int64_t N, int64_t K, c
     behind.bias = ahead(e.bias, n, e.bias_type);
     behind.residual = ahead(e.residual, n, e.residual_type);
     behind.z = static_cast<float*>(ahead(e.z, n, FP4_TYPE_F32));
-    return run_epilogue(plan_of(M, N - n, K, fp4_device_cus(), false), out_type, M, N - n, K, a, rest, behind, ahead(y, n, out_type), ldy,
+    return run_epilogue(plan_with(M, N - n, K, e, false), out_type, M, N - n, K, a, rest, behind, ahead(y, n, out_type), ldy,
                         nullptr, 0, st);
   }
   Args g{};
@@ -60,7 +65,7 @@ extern "C" int w4a4_matmul_epilogue(int out_type, int64_t M, int64_t N, int64_t 
   if (int rc = check_operand(b, K)) return rc;
   if (int rc = check_output(out_type, N, y, ldy)) return rc;
   if (workspace && !fp4_aligned(workspace, 16)) return FP4_ERR_ALIGN;
-  return run_epilogue(plan_of(M, N, K, fp4_device_cus()), out_type, M, N, K, *a, *b, *epilogue, y, ldy, workspace, workspace_bytes,
+  return run_epilogue(plan_with(M, N, K, *epilogue), out_type, M, N, K, *a, *b, *epilogue, y, ldy, workspace, workspace_bytes,
                       static_cast<hipStream_t>(stream));
 }
 
@@ -77,7 +82,7 @@ extern "C" int w4a4_linear_epilogue(int x_type, int out_type, int64_t M, int64_t
   if (workspace && !fp4_aligned(workspace, 16)) return FP4_ERR_ALIGN;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (fused(M, N, K)) return launch_rows(x_type, out_type, (int)M, (int)N, (int)K, x, ldx, nullptr, *b, y, ldy, st, epilogue);
-  const Plan p = plan_of(M, N, K, fp4_device_cus());
+  const Plan p = plan_with(M, N, K, *epilogue);
   const LinearSpace sp = linear_space(p, M, K);
   if (!workspace || workspace_bytes < (size_t)(sp.q + sp.s)) return FP4_ERR_ARG;
   auto* w = static_cast<uint8_t*>(workspace);

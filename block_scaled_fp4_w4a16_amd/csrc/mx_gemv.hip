@@ -194,12 +194,7 @@ __global__ void __launch_bounds__(64 * GV_MAX_WAVES)
     const int i = base + lane;
     int lo = i < groups.E ? bound_at(groups, i, T) : 0, hi = i < groups.E ? bound_at(groups, i + 1, T) : 0;
     if (base == 0) first = uniform(lo);
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int l = __shfl_up(lo, d), h = __shfl_up(hi, d);
-      if (lane >= d) lo = max(lo, l), hi = max(hi, h);
-    }
-    lo = max(lo, most), hi = max(max(hi, lo), most);
+    lo = max(scan_max(lo), most), hi = max(scan_max(hi), lo);
     const bool here = i < groups.E && hi > lo;
     const uint64_t some = __builtin_amdgcn_ballot_w64(here);
     const int rank = seen + __builtin_popcountll(some & ((1ull << lane) - 1));

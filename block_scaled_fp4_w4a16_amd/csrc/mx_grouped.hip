@@ -21,8 +21,8 @@ static int run_grouped(int out_type, int64_t T, int64_t N, int64_t K, const fp4_
   p.a = a, p.b = b, p.y = y, p.ldy = ldy, p.M = (int)T, p.N = (int)N, p.K = (int)K, p.fill = fill, p.groups = g;
   p.step_q = step_q, p.step_s = step_s;
   if (e) p.epi = *e;
-  p.tiles_n = (int)((N + tile - 1) / tile);
-  return launch_out<ROWS>(out_type, tile, p, most_tiles(T, g.E, tile) * p.tiles_n, st);
+  p.tiles_n = (int)((N + tile_columns(tile) - 1) / tile_columns(tile));
+  return launch_out<ROWS>(out_type, tile, p, most_tiles(T, g.E, tile_rows(tile)) * p.tiles_n, st);
 }
 
 static bool grouped_fused(int64_t T, int64_t N, int64_t K, int64_t E) {

@@ -25,33 +25,44 @@ __device__ __forceinline__ int bound_at(const Groups& g, int e, int T) {
   return (int)(v < 0 ? 0 : v > T ? T : v);
 }
 
+// Inclusive scans over the wave's lanes, of values that are not negative: within rows of 16, then rows 1 and 3 take the last of
+// the row before, rows 2 and 3 the last of the first half. A few cycles a step, where exchanges through LDS take a hundred.
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ int from_lane(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, ROWS == 0xf);
+}
+constexpr int DPP_ROW_SHR = 0x110, DPP_WAVE_SHR1 = 0x138, DPP_ROW_BCAST15 = 0x142, DPP_ROW_BCAST31 = 0x143;
+template <class F>
+__device__ __forceinline__ int scan(int v, F op) {
+  v = op(v, from_lane<DPP_ROW_SHR + 1>(v));
+  v = op(v, from_lane<DPP_ROW_SHR + 2>(v));
+  v = op(v, from_lane<DPP_ROW_SHR + 4>(v));
+  v = op(v, from_lane<DPP_ROW_SHR + 8>(v));
+  v = op(v, from_lane<DPP_ROW_BCAST15, 0xa>(v));
+  return op(v, from_lane<DPP_ROW_BCAST31, 0xc>(v));
+}
+__device__ __forceinline__ int scan_max(int v) {
+  return scan(v, [](int a, int b) { return max(a, b); });
+}
+__device__ __forceinline__ int scan_sum(int v) {
+  return scan(v, [](int a, int b) { return a + b; });
+}
+
 // Fills the tables (one wave; the caller's barrier makes them visible). Bounds that decrease count as the largest in front of
 // them, so that groups never overlap and their rows are T at most.
 template <int UNIT_ROWS>
 __device__ __forceinline__ void read_groups(const Groups& g, int T, int* start, int* units, int lane) {
-  int most = 0, sum = 0, last = 0;
+  int most = 0, sum = 0;
   for (int base = 0; base <= g.E; base += 64) {
     const int e = base + lane;
-    int v = e <= g.E ? bound_at(g, e, T) : 0;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int o = __shfl_up(v, d);
-      if (lane >= d) v = max(v, o);
-    }
-    v = max(v, most);
+    const int v = max(scan_max(e <= g.E ? bound_at(g, e, T) : 0), most);
     // the units of group e - 1, which ends here; the first lane's began in the 64 bounds before
-    int before = __shfl_up(v, 1);
-    if (lane == 0) before = base ? last : v;
-    int n = (v - before + UNIT_ROWS - 1) / UNIT_ROWS;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int o = __shfl_up(n, d);
-      if (lane >= d) n += o;
-    }
-    n += sum;
+    int before = from_lane<DPP_WAVE_SHR1>(v);
+    if (lane == 0) before = base ? most : v;
+    const int n = scan_sum((v - before + UNIT_ROWS - 1) / UNIT_ROWS) + sum;
     if (e <= g.E) start[e] = v, units[e] = n;
-    most = last = __shfl(v, 63);
-    sum = __shfl(n, 63);
+    most = __builtin_amdgcn_readlane(v, 63);
+    sum = __builtin_amdgcn_readlane(n, 63);
   }
 }
 

@@ -40,7 +40,7 @@ inline double tiles_us(const TileCost& c, int64_t work, int stages, int cus) {
 // K = 9728: tiles of 64 take 13.1 us, of 128 28.9 us; 64 x 2560, K = 9728: 12.8 us, in 4 parts 9.3 us.
 // Where the last round of tiles of 256 would be a small one (split), the columns that fill whole rounds are one product and
 // the others a second in tiles that fill the device.
-inline Plan plan_of(int64_t M, int64_t N, int64_t K, int cus, bool split = true) {
+inline Plan plan_of(int64_t M, int64_t N, int64_t K, int cus, bool split = true, const TileCost* costs = TILE_COSTS) {
   Plan p{};
   p.ldp = (N + 3) / 4 * 4;
   const int stages = stages_of(K);
@@ -52,7 +52,8 @@ inline Plan plan_of(int64_t M, int64_t N, int64_t K, int cus, bool split = true)
   // columns with a long K take longer (1 x 16 x 2^20: 216 us, where 17 rows in K parts take 70; 16 x 128 x 65536: 16.8, 12.7)
   if (M <= 16) p.us = 1.8 + (double)((N + 15) / 16) * stages * (0.00034 + 0.00001 * M);
   const double least = 3.5 + N * K * (17 / 32.) / 5e6;  // the weights' bytes at 5 TB/s
-  for (const TileCost& c : TILE_COSTS) {
+  for (int i = 0; i < 3; ++i) {
+    const TileCost& c = costs[i];
     const int64_t tiles = ((M + c.tile - 1) / c.tile) * ((N + c.tile - 1) / c.tile);
     for (int want = 1; want <= 16; want *= 2) {
       const int per = ((stages + want - 1) / want + 1) & ~1, parts = (stages + per - 1) / per;
@@ -64,10 +65,10 @@ inline Plan plan_of(int64_t M, int64_t N, int64_t K, int cus, bool split = true)
     }
   }
   if (split) {
-    const TileCost& c = TILE_COSTS[2];
+    const TileCost& c = costs[2];
     const int64_t down = (M + 255) / 256, across = (N + 255) / 256, fit = down * across / cus * cus / down;
     if (fit > 0 && fit < across) {
-      const Plan rest = plan_of(M, N - fit * 256, K, cus, false);
+      const Plan rest = plan_of(M, N - fit * 256, K, cus, false, costs);
       const double us = tiles_us(c, down * fit, (stages + 1) & ~1, cus) + rest.us;
       if (rest.parts == 1 && us < 0.95 * p.us)
         p.us = us, p.tile = 256, p.parts = 1, p.per = (stages + 1) & ~1, p.first_n = fit * 256;
@@ -86,27 +87,55 @@ inline bool fused(int64_t M, int64_t N, int64_t K) {
   return M <= 16 && (N + 15) / 16 * stages_of(K) * (M + 3) <= 32768;
 }
 
+// The figures of tiles with an epilogue: what it adds to each round, as measured at 8192 x 14336 x 4096 and 8192 x 9728 x 2560. The
+// matrix core idles through it in tiles of 256, one of which fits a unit; tiles of 128 cover each other's. So gelu onto a
+// residual at 8192 x 9728 x 2560 takes 226 us in tiles of 256 and 203 in tiles of 128, a bias alone 124 and 130; at
+// 14336 x 4096 382 and 399, 270 and 327.
+struct EpilogueCosts {
+  TileCost of[3];
+};
+inline EpilogueCosts epilogue_costs(bool erf, bool other_activation, bool residual, bool z) {
+  EpilogueCosts e{{TILE_COSTS[0], TILE_COSTS[1], TILE_COSTS[2]}};
+  const double more[3] = {0.3 + (erf ? 0.8 : other_activation ? 0.3 : 0) + (residual ? 1 : 0) + (z ? 2 : 0),
+                          1.5 + (erf ? 2.5 : other_activation ? 0.7 : 0) + (residual ? 4.5 : 0) + (z ? 9 : 0),
+                          5.0 + (erf ? 8 : other_activation ? 3 : 0) + (residual ? 9 : 0) + (z ? 13 : 0)};
+  for (int i = 0; i < 3; ++i) e.of[i].launch += more[i], e.of[i].round += more[i];
+  return e;
+}
+
+// Tiles of rows in groups: 64, 64 x 128 (WIDE; few rows of many groups, bound by the weights' bytes), 128 and 256 square. All but
+// those of 64 are taken as streams, so that a round costs its stages and its way out; those of 64, which have more stages on
+// their way, are for what leaves units idle (200 rows in 8 groups, 1024 columns, K = 2560: 7.8 us, in 64 x 128 12.9).
+constexpr int WIDE = 96;
+inline int tile_rows(int tile) { return tile == WIDE ? 64 : tile; }
+inline int tile_columns(int tile) { return tile == WIDE ? 128 : tile; }
+constexpr TileCost GROUPED_COSTS[] = {{64, 5, 4, 0.27, 0.5}, {WIDE, 6.3, 2.3, 0.6, 0.95}, {128, 9, 5, 0.8, 1.25}, {256, 17, 13, 1.75, 0}};
+constexpr TileCost GRADIENT_COSTS[] = {{128, 7.5, 3.5, 0.8, 1.25}, {256, 11, 7, 1.75, 0}};
+
 // The tiles of a product of T rows in E groups, whose sizes only the device knows, with N columns and depth K: the cheapest
-// by the figures above for groups of equal size, each of which ends inside a tile. 0: rows_grouped_kernel, for up to 16 rows.
+// by those figures for groups of equal size, each of which ends inside a tile. 0: rows_grouped_kernel, for up to 16 rows.
+// Measured in tiles of 64 x 128, 128 and 256, in us: 512 rows in 64 groups, 2560 columns, K = 1024: 19.6, 23, 36; 4000 in 32, 2560,
+// 2560: 39.5, 36, 61; 8192 in 16, 4096, 2560: 98, 82, 89; 16384 in 8, 14336, 4096: 1027, 775, 593.
 inline int grouped_tile(int64_t T, int64_t N, int64_t K, int64_t E, int cus) {
   if (T <= 16) return 0;
   const double some = E < T ? E : T, each = T / some, least = 3.5 + some * N * K * (17 / 32.) / 5e6;
   int tile = 0;
   double best = 1e30;
-  for (const TileCost& c : TILE_COSTS) {
-    const double down = each / c.tile + 0.5, rows = some * (down > 1 ? down : 1);
-    double us = tiles_us(c, (int64_t)(rows * ((N + c.tile - 1) / c.tile)), (stages_of(K) + 1) & ~1, cus);
+  for (const TileCost& c : GROUPED_COSTS) {
+    const double down = each / tile_rows(c.tile) + 0.5, rows = some * (down > 1 ? down : 1);
+    double us = tiles_us(c, (int64_t)(rows * ((N + tile_columns(c.tile) - 1) / tile_columns(c.tile))), (stages_of(K) + 1) & ~1, cus);
     if (us < least) us = least;
     if (us < best) best = us, tile = c.tile;
   }
   return tile;
 }
 
-// The tiles of E products of M x N outputs that contract T rows between them.
+// The tiles of E products of M x N outputs that contract T rows between them. 8192 rows, 16 of 4096 x 2560: 150 us in tiles of
+// 128, 134 in tiles of 256; 200 rows, 8 of 1024 x 2560 in FP32: 24 and 35.
 inline int gradient_tile(int64_t T, int64_t M, int64_t N, int64_t E, int cus) {
   int tile = 0;
   double best = 1e30;
-  for (const TileCost& c : TILE_COSTS) {
+  for (const TileCost& c : GRADIENT_COSTS) {
     const int64_t tiles = E * ((M + c.tile - 1) / c.tile) * ((N + c.tile - 1) / c.tile);
     const double us = tiles_us(c, tiles, (stages_of((T + E - 1) / E) + 1) & ~1, cus);
     if (us < best) best = us, tile = c.tile;

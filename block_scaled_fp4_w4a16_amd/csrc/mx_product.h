@@ -99,7 +99,7 @@ __device__ __forceinline__ void read_part(uint32_t out, f32x4 (&v)[N]) {
 // How a wave's sums leave: in parts of 16 rows and COLS columns.
 template <int OUT, class G>
 struct Way {
-  static constexpr int SPLIT = G::TN == 8 ? 2 : 1, COLS = 16 * G::TN / SPLIT, STRIDE = COLS * 4 + 16, ALL = G::TM * SPLIT;
+  static constexpr int SPLIT = G::NBUF == 2 ? 2 : 1, COLS = 16 * G::TN / SPLIT, STRIDE = COLS * 4 + 16, ALL = G::TM * SPLIT;
   static constexpr int W = OUT == FP4_TYPE_F32 ? 4 : 8;                     // columns of a lane
   static constexpr int PER = COLS / W, ROWS = 64 / PER, STEPS = 16 / ROWS;  // lanes per row, rows per step
   static constexpr int READS = STEPS * W / 4;                               // of 16 bytes, per lane and part
@@ -214,6 +214,81 @@ __device__ __forceinline__ void store_whole(const f32x4 (&acc)[G::TM][G::TN], co
   }
 }
 
+// Row tile I of a wave's sums to v (a branch finds it, as in stage_any).
+template <int I, class G>
+__device__ __forceinline__ void take_sums(const f32x4 (&acc)[G::TM][G::TN], f32x4 (&v)[G::TN]) {
+#pragma unroll
+  for (int j = 0; j < G::TN; ++j) {
+    v[j] = acc[I][j];
+    asm volatile("; row tile %1" : "+v"(v[j]) : "n"(I));
+  }
+}
+template <int FROM, int TO, class G>
+__device__ __forceinline__ void take_any(int i, const f32x4 (&acc)[G::TM][G::TN], f32x4 (&v)[G::TN]) {
+  if constexpr (TO - FROM == 1) {
+    take_sums<FROM, G>(acc, v);
+  } else {
+    constexpr int MID = (FROM + TO) / 2;
+    if (i < MID) take_any<FROM, MID, G>(i, acc, v);
+    else take_any<MID, TO, G>(i, acc, v);
+  }
+}
+
+// store_whole for 16-bit y without residual and z: everything is done where the sums are, four columns of a row to a lane, and
+// goes through LDS rounded, whole rows of the wave's columns at a time.
+template <int OUT, class G>
+__device__ __forceinline__ void store_rounded(const f32x4 (&acc)[G::TM][G::TN], const fp4_epilogue& epi, int64_t bias_at, void* y,
+                                              int64_t ldy, int row0, int rows, int col0, int lane, uint8_t* stage) {
+  constexpr int COLS = 16 * G::TN, STRIDE = COLS * 2 + 16, PER = COLS / 8, ROWS = 64 / PER, STEPS = 16 / ROWS, TN = G::TN;
+  const int n = lane & 15, g = lane >> 4, r = lane / PER, c = lane % PER * 8;
+  const uint32_t in = lds_address(stage) + n * STRIDE + 8 * g, out = lds_address(stage) + r * STRIDE + 2 * c;
+  const auto to = fp4::make_rsrc(static_cast<uint8_t*>(y) + (row0 * ldy + col0) * 2, (uint32_t)(((rows - 1) * (int)ldy + COLS) * 2));
+  float bias[TN][4];
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bias[j][e] = 0;
+    if (epi.bias) values_of(epi.bias_type, load_raw<4>(epi.bias_type, epi.bias, bias_at + col0 + 16 * j + 4 * g, 4), bias[j]);
+  }
+  const int all = min(G::TM, (rows + 15) / 16);
+#pragma unroll 1
+  for (int i = 0; i < all; ++i) {
+    f32x4 v[TN];
+    take_any<0, G::TM, G>(i, acc, v);
+    float f[4 * TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[4 * j + e] = v[j][e] + bias[j][e];
+    activate(epi.activation, f);
+    u32x2 h[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) h[j] = u32x2{pack2<OUT>(f[4 * j], f[4 * j + 1]), pack2<OUT>(f[4 * j + 2], f[4 * j + 3])};
+    asm volatile("ds_write_b64 %0, %1\n\tds_write_b64 %0, %2 offset:32" : : "v"(in), "v"(h[0]), "v"(h[1]) : "memory");
+    if constexpr (TN >= 4) asm volatile("ds_write_b64 %0, %1 offset:64\n\tds_write_b64 %0, %2 offset:96" : : "v"(in), "v"(h[2]), "v"(h[3]) : "memory");
+    if constexpr (TN == 8)
+      asm volatile("ds_write_b64 %0, %1 offset:128\n\tds_write_b64 %0, %2 offset:160\n\tds_write_b64 %0, %3 offset:192\n\t"
+                   "ds_write_b64 %0, %4 offset:224"
+                   :
+                   : "v"(in), "v"(h[4]), "v"(h[5]), "v"(h[6]), "v"(h[7])
+                   : "memory");
+    const uint32_t at = (uint32_t)(((16 * i + r) * (int)ldy + c) * 2), step = ROWS * (int)ldy * 2;
+    if constexpr (STEPS == 1) {
+      f32x4 o;
+      asm volatile("ds_read_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(o) : "v"(out) : "memory");
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), to, at, 0, 0);
+    } else {
+      f32x4 o[STEPS];
+      read_part<STEPS, ROWS * STRIDE, 2 * ROWS * STRIDE, 3 * ROWS * STRIDE>(out, o);
+#pragma unroll
+      for (int k = 0; k < STEPS; ++k) {
+        const f32x4 x = o[k];
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), to, at + k * step, 0, 0);
+      }
+    }
+  }
+}
+
 // The same where columns end inside the tile, or rows lie at any alignment: accesses of what is there.
 template <int OUT, class G>
 __device__ __forceinline__ void store_part(const f32x4 (&acc)[G::TM][G::TN], const fp4_epilogue& epi, int64_t bias_at, void* y,
@@ -263,7 +338,8 @@ __device__ __forceinline__ void store_epilogue(const f32x4 (&acc)[G::TM][G::TN],
     store_part<OUT, G>(acc, epi, bias_at, y, ldy, row0, rows, col0, N, lane, stage);
   } else if (!epi.residual) {
     if (epi.z) MX_WHOLE(0, true);
-    else MX_WHOLE(0, false);
+    else if constexpr (OUT == FP4_TYPE_F32) MX_WHOLE(0, false);
+    else store_rounded<OUT, G>(acc, epi, bias_at, y, ldy, row0, rows, col0, lane, stage);
   } else if (epi.residual_type == FP4_TYPE_F32) {
     if (epi.z) MX_WHOLE(2, true);
     else MX_WHOLE(2, false);
@@ -284,9 +360,12 @@ __device__ __forceinline__ void fill_row(const fp4_epilogue& epi, void* y, int64
   }
 }
 
-// Whether a workgroup takes several tiles: tiles of which one fits a compute unit. (The others overlap by sharing a unit.)
+// Whether a workgroup takes several tiles, one's last stages loading the next one's first: with two buffers, which every tile
+// begins alike.
 template <class G>
-constexpr bool STREAMED = G::NBUF == 2 && G::LDS > 80 * 1024;
+constexpr bool STREAMED = G::NBUF == 2;
+template <class G>
+constexpr int PER_UNIT = G::LDS > 80 * 1024 ? 1 : 2;  // workgroups that fit a compute unit
 
 template <class G, int OUT, Mode MODE>
 __global__ void __launch_bounds__(G::THREADS, G::LDS > 80 * 1024 ? G::WAVES / 4 : G::WAVES / 2) product_kernel(Args p) {
@@ -336,8 +415,16 @@ __global__ void __launch_bounds__(G::THREADS, G::LDS > 80 * 1024 ? G::WAVES / 4 
   // tile `id`. Workgroups go round-robin over the 8 XCDs: XCD x takes a contiguous run of the tiles.
   const auto piece_of = [&](int id) {
     Piece j;
-    const int xcds = 8, x = id % xcds, q = total / xcds, r = total % xcds;
+    const int xcds = 8, x = id % xcds, whole = p.tiles_m * p.tiles_n, q = total / xcds, r = total % xcds;
     int t = x * q + min(x, r) + id / xcds, tm, tn;  // bijective for any total
+    if constexpr (MODE == DEPTH) {
+      // groups differ in their tiles' work: each one's are spread over the XCDs, in runs where they divide evenly
+      t = id;
+      if (whole % xcds == 0) {
+        const int run = whole / xcds, e = id / whole;
+        t = e * whole + x * run + (id - e * whole) / xcds;
+      }
+    }
     j.e = j.from = 0, j.end = p.M, j.nb = (int)blocks_of(p.K);
     int first = 0, tiles_m = p.tiles_m;
     if constexpr (MODE == ROWS) {
@@ -347,9 +434,8 @@ __global__ void __launch_bounds__(G::THREADS, G::LDS > 80 * 1024 ? G::WAVES / 4 
       tiles_m = uniform(units[j.e + 1]) - before;
       first = uniform(start[j.e]), j.end = uniform(start[j.e + 1]);
     } else if constexpr (MODE == DEPTH) {
-      const int tiles = p.tiles_m * p.tiles_n;
-      j.e = t / tiles;
-      t -= j.e * tiles;
+      j.e = t / whole;
+      t -= j.e * whole;
       j.nb = (uniform(start[j.e + 1]) - uniform(start[j.e]) + BLOCK - 1) / BLOCK;
       j.from = uniform(units[j.e]) * (UNIT / BLOCK);
     }
@@ -453,7 +539,7 @@ static int launch_product(Args p, int64_t tiles, hipStream_t st) {
   static Fp4LdsLimit limit;
   const int lds = G::LDS + (MODE == DENSE ? 0 : group_table_bytes(p.groups.E));
   limit.ensure(reinterpret_cast<const void*>(&product_kernel<G, OUT, MODE>), G::LDS + (MODE == DENSE ? 0 : group_table_bytes(MAX_GROUPS)));
-  const int units = fp4_device_cus() & ~7;  // a multiple of the 8 XCDs: a workgroup's tiles stay on its XCD
+  const int units = PER_UNIT<G> * (fp4_device_cus() & ~7);  // a multiple of the 8 XCDs: a workgroup's tiles stay on its XCD
   const int64_t wgs = STREAMED<G> && units > 0 && tiles > units ? units : tiles;
   if (tiles > (1LL << 30) || !fits_launch(wgs, G::THREADS)) return FP4_ERR_UNSUPPORTED;
   return fp4_launch(product_kernel<G, OUT, MODE>, dim3((unsigned)wgs), dim3(G::THREADS), lds, st, p);
@@ -462,14 +548,18 @@ static int launch_product(Args p, int64_t tiles, hipStream_t st) {
 using Tile256 = Tile<256, 256, 2, 2, 2, 1>;
 using Tile128 = Tile<128, 128, 2, 2, 2, 1>;
 using Tile64 = Tile<64, 64, 2, 2, 4, 2>;
-static_assert(Tile256::STAGE >= 16 * (64 * 4 + 16), "a wave's staging rows of 64 FP32 sums");
+using TileWide = Tile<64, 128, 2, 2, 2, 1>;
+static_assert(Tile256::STAGE >= 16 * (64 * 4 + 16) && Tile128::STAGE >= 16 * (32 * 4 + 16), "a wave's staging rows of FP32 sums");
 static_assert(Tile256::LDS + group_table_bytes(MAX_GROUPS) <= 160 * 1024, "");
 
 template <int OUT, Mode MODE>
 static int launch_tile(int tile, const Args& p, int64_t tiles, hipStream_t st) {
   if (tile == 256) return launch_product<Tile256, OUT, MODE>(p, tiles, st);
-  if (tile == 128) return launch_product<Tile128, OUT, MODE>(p, tiles, st);
-  return launch_product<Tile64, OUT, MODE>(p, tiles, st);
+  if constexpr (MODE != DEPTH)
+    if (tile == 64) return launch_product<Tile64, OUT, MODE>(p, tiles, st);
+  if constexpr (MODE == ROWS)
+    if (tile == WIDE) return launch_product<TileWide, OUT, MODE>(p, tiles, st);
+  return launch_product<Tile128, OUT, MODE>(p, tiles, st);
 }
 template <Mode MODE>
 static int launch_out(int out_type, int tile, const Args& p, int64_t tiles, hipStream_t st) {

@@ -30,7 +30,7 @@ struct Tile {
   // direct loads of a thread that may be on their way when a stage has to be there: those of the NBUF - 2 stages
   // behind the next one (with SG 1 half of them bring scales too)
   static constexpr int BEHIND = (NBUF - 2) * SLOTS + (SG == 2 ? 0 : (NBUF / 2 - 1) * SSLOTS);
-  static_assert((SG == 1 || (SG == 2 && NBUF == 4)) && (NBUF == 2 || NBUF == 4) && BEHIND + SLOTS < 64 && BM % (8 * WAVES) == 0 && ROWS * SG % THREADS == 0, "");
+  static_assert((SG == 1 || (SG == 2 && NBUF == 4)) && (NBUF == 2 || NBUF == 4) && BEHIND + SLOTS < 64 && BM % (8 * WAVES) == 0 && ROWS % 64 == 0 && (NBUF == 2 || ROWS * SG % THREADS == 0), "");
 };
 
 __device__ __forceinline__ int swizzle(int row) { return row & 7; }
@@ -80,6 +80,7 @@ __device__ __forceinline__ void issue_scales(const Sources& src, uint8_t* buf, u
 #pragma unroll
   for (int i = 0; i < G::SSLOTS; ++i) {
     const int first = (G::WAVES * i + wave) * (64 / G::SG);
+    if (G::ROWS * G::SG % G::THREADS && first >= G::ROWS) break;  // the last waves have none (NBUF 2: no wait counts them)
     const int row = first + lane / G::SG;
     const uint32_t at = from + (G::SG == 2 ? ((lane ^ row >> 3) & 1) * 16 : 0);
     auto* to = (__attribute__((address_space(3))) void*)(buf + first * 16 * G::SG);
