@@ -422,7 +422,6 @@ Tensor dequant_new(const Tensor& codes, const Tensor& scales, int64_t rows, int6
 // A residual [M, N] whose rows are contiguous (a copy only where its strides ask for one).
 OptTensor residual_rows(const OptTensor& residual, int64_t M, int64_t N) {
   if (!residual) return residual;
-  no_gradient(*residual, "residual");
   if (residual->dim() != 2 || residual->size(0) != M || residual->size(1) != N)
     value_error("residual must have shape [", M, ", ", N, "], not ", residual->sizes());
   return as_rows(*residual);
@@ -433,6 +432,7 @@ Tensor matmul_new(const Tensor& aq, const Tensor& as, int64_t M, const Tensor& b
                   const std::optional<std::string>& activation, const OptTensor& residual) {
   refuse_tracing();
   if (out) no_gradient(*out, "the output");
+  no_gradient(epilogue_of(bias, activation, residual));
   const OnStream on(stream, one_device({&bq, &bs}));
   const OptTensor r = residual_rows(residual, M, N);
   Tensor y = output_of(out, M, N, dtype, bq.device());
@@ -446,6 +446,7 @@ Tensor linear_new(const Tensor& x, const Tensor& bq, const Tensor& bs, int64_t N
   refuse_tracing();
   no_gradient(x, "x");
   if (out) no_gradient(*out, "the output");
+  no_gradient(epilogue_of(bias, activation, residual));
   if (x.dim() != 2) value_error("x must be [M, K] with the weights' K");
   if (x.size(1) != K) value_error("depths differ: ", x.size(1), " and ", K);
   const OnStream on(stream, one_device({&x, &bq, &bs}));
@@ -468,6 +469,7 @@ Tensor grouped_matmul_new(const Tensor& aq, const Tensor& as, int64_t T, const T
                           const OptTensor& bias, const std::optional<std::string>& activation, const OptTensor& residual) {
   refuse_tracing();
   if (out) no_gradient(*out, "the output");
+  no_gradient(epilogue_of(bias, activation, residual));
   const int64_t N = rows_per_group(rows, offsets);
   const OnStream on(stream, one_device({&bq, &bs}));
   const OptTensor r = residual_rows(residual, T, N);
@@ -482,6 +484,7 @@ Tensor grouped_linear_new(const Tensor& x, const Tensor& bq, const Tensor& bs, i
   refuse_tracing();
   no_gradient(x, "x");
   if (out) no_gradient(*out, "the output");
+  no_gradient(epilogue_of(bias, activation, residual));
   if (x.dim() != 2) value_error("x must be [T, K] with the weights' K");
   if (x.size(1) != K) value_error("depths differ: ", x.size(1), " and ", K);
   const int64_t N = rows_per_group(rows, offsets);

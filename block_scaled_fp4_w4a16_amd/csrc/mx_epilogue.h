@@ -57,22 +57,22 @@ __device__ __forceinline__ void activate(int act, float (&z)[W]) {
   }
 }
 
-// f'(z). |z| is held where f' has long been 0 or 1 in FP32 (a NaN stays), so that infinities get their limits.
+// f'(z). |z| is held where f' has long been 0 or 1 in FP32 (a NaN stays), so that infinities get their limits. With s the logistic
+// function, 1 - s is taken as 2^u s: by a subtraction, an s that rounds to 1 less a bit or two would be z times that off.
 __device__ __forceinline__ float slope(int act, float z) {
   if (act == FP4_ACT_RELU) return z > 0 ? 1.0f : z <= 0 ? 0.0f : z;
   z = z > 128.0f ? 128.0f : z < -128.0f ? -128.0f : z;
-  if (act == FP4_ACT_SILU) {
-    const float s = silu_factor(z);
-    return s + z * s * (1.0f - s);
+  if (act == FP4_ACT_SILU || act == FP4_ACT_GELU_TANH) {
+    const bool silu = act == FP4_ACT_SILU;
+    const float zz = z * z, u = z * (silu ? -LOG2E : -LOG2E * TANH_1 - LOG2E * TANH_3 * zz);
+    const float e = __builtin_amdgcn_exp2f(fminf(u, 120.0f)), s = __builtin_amdgcn_rcpf(1.0f + e);
+    const float d = z * s * (e * s) * (silu ? 1.0f : TANH_1 + 3.0f * TANH_3 * zz);
+    return s + d;
   }
   if (act == FP4_ACT_GELU) {
     float e;
     const float tail = normal_tail(z, e);
     return (z < 0 ? tail : 1.0f - tail) + z * e * 0.398942280f;
-  }
-  if (act == FP4_ACT_GELU_TANH) {
-    const float s = tanh_factor(z);
-    return s + z * s * (1.0f - s) * (TANH_1 + 3.0f * TANH_3 * z * z);
   }
   return 1.0f;
 }

@@ -207,10 +207,11 @@ __global__ void __launch_bounds__(64 * GV_MAX_WAVES)
     seen += __builtin_popcountll(some);
     most = __builtin_amdgcn_readlane(hi, 63);
   }
-  if (fill && blockIdx.y == 0 && (int)threadIdx.x < 256) {
-    const int r = threadIdx.x >> 4, c = n0 + (threadIdx.x & 15);
-    if (r < first + T - most && c < N) {
-      const int64_t row = row_outside(r, first, most);
+  if (fill && blockIdx.y == 0) {
+    for (int i = threadIdx.x; i < 16 * (first + T - most); i += blockDim.x) {
+      const int c = n0 + (i & 15);
+      if (c >= N) continue;
+      const int64_t row = row_outside(i >> 4, first, most);
       float f[1] = {0};
       if (epi.residual) values_of(epi.residual_type, load_raw<1>(epi.residual_type, epi.residual, row * epi.ldr + c, 1), f);
       store_values(out_type, y, row * ldy + c, f, 1);
