@@ -23,7 +23,7 @@ struct Args {
   int64_t ldy;
   int M, N, K;            // DEPTH: K rows in groups
   int tiles_m, tiles_n;   // ROWS: tiles_m is not known
-  int whole;              // rows of y, z and the residual suit store_whole
+  int whole;              // as store_epilogue takes it
   int fill;               // ROWS: rows of no group become the residual, or zero
   fp4_epilogue epi;
   Groups groups;
@@ -130,19 +130,23 @@ __device__ __forceinline__ Raw<W> buffer_raw(__amdgpu_buffer_rsrc_t r, uint32_t 
   }
   return v;
 }
+// 16 bytes out; `past`: marked as not to be kept in the caches.
+__device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t r, uint32_t at, const u32x4& x, bool past) {
+  if (past) __builtin_amdgcn_raw_buffer_store_b128(x, r, at, 0, 2);
+  else __builtin_amdgcn_raw_buffer_store_b128(x, r, at, 0, 0);
+}
 template <int OUT, int W>
-__device__ __forceinline__ void buffer_store(__amdgpu_buffer_rsrc_t r, uint32_t at, const float (&f)[W]) {
+__device__ __forceinline__ void buffer_store(__amdgpu_buffer_rsrc_t r, uint32_t at, const float (&f)[W], bool past) {
   if constexpr (OUT == FP4_TYPE_F32) {
 #pragma unroll
     for (int i = 0; i < W / 4; ++i) {
       u32x4 x;
       __builtin_memcpy(&x, f + 4 * i, 16);
-      __builtin_amdgcn_raw_buffer_store_b128(x, r, at + 16 * i, 0, 0);
+      put(r, at + 16 * i, x, past);
     }
   } else {
     static_assert(W == 8, "");
-    __builtin_amdgcn_raw_buffer_store_b128(
-        u32x4{pack2<OUT>(f[0], f[1]), pack2<OUT>(f[2], f[3]), pack2<OUT>(f[4], f[5]), pack2<OUT>(f[6], f[7])}, r, at, 0, 0);
+    put(r, at, u32x4{pack2<OUT>(f[0], f[1]), pack2<OUT>(f[2], f[3]), pack2<OUT>(f[4], f[5]), pack2<OUT>(f[6], f[7])}, past);
   }
 }
 
@@ -151,7 +155,7 @@ __device__ __forceinline__ void buffer_store(__amdgpu_buffer_rsrc_t r, uint32_t 
 // many a residual has behind it: it is asked for U parts ahead and waits for no store that is younger.
 template <int OUT, class G, int RES, bool Z>
 __device__ __forceinline__ void store_whole(const f32x4 (&acc)[G::TM][G::TN], const fp4_epilogue& epi, int64_t bias_at, void* y,
-                                            int64_t ldy, int row0, int rows, int col0, int lane, uint8_t* stage) {
+                                            int64_t ldy, int row0, int rows, int col0, int lane, uint8_t* stage, bool past) {
   using P = Way<OUT, G>;
   constexpr int W = P::W, U = P::ALL < 4 ? P::ALL : 4, EB = elem_bytes(OUT), RB = RES == 2 ? 4 : 2, WIDTH = P::COLS * P::SPLIT;
   const int n = lane & 15, g = lane >> 4, r = lane / P::PER, c = lane % P::PER * W;
@@ -199,7 +203,7 @@ __device__ __forceinline__ void store_whole(const f32x4 (&acc)[G::TM][G::TN], co
         __builtin_memcpy(f, v + k * (W / 4), 4 * W);
 #pragma unroll
         for (int i = 0; i < W; ++i) f[i] += bias[u % P::SPLIT][i];
-        if constexpr (Z) buffer_store<FP4_TYPE_F32>(keep, place(s, k, epi.ldz, 4), f);
+        if constexpr (Z) buffer_store<FP4_TYPE_F32>(keep, place(s, k, epi.ldz, 4), f, past);
         activate(epi.activation, f);
         if constexpr (RES != 0) {
           float add[W];
@@ -208,7 +212,7 @@ __device__ __forceinline__ void store_whole(const f32x4 (&acc)[G::TM][G::TN], co
           for (int i = 0; i < W; ++i) f[i] += add[i];
           ahead[u][k] = buffer_raw<RES == 2, W>(from, place(s + U, k, epi.ldr, RB));  // past the tile: nothing
         }
-        buffer_store<OUT>(to, place(s, k, ldy, EB), f);
+        buffer_store<OUT>(to, place(s, k, ldy, EB), f, past);
       }
     }
   }
@@ -238,7 +242,7 @@ __device__ __forceinline__ void take_any(int i, const f32x4 (&acc)[G::TM][G::TN]
 // goes through LDS rounded, whole rows of the wave's columns at a time.
 template <int OUT, class G>
 __device__ __forceinline__ void store_rounded(const f32x4 (&acc)[G::TM][G::TN], const fp4_epilogue& epi, int64_t bias_at, void* y,
-                                              int64_t ldy, int row0, int rows, int col0, int lane, uint8_t* stage) {
+                                              int64_t ldy, int row0, int rows, int col0, int lane, uint8_t* stage, bool past) {
   constexpr int COLS = 16 * G::TN, STRIDE = COLS * 2 + 16, PER = COLS / 8, ROWS = 64 / PER, STEPS = 16 / ROWS, TN = G::TN;
   const int n = lane & 15, g = lane >> 4, r = lane / PER, c = lane % PER * 8;
   const uint32_t in = lds_address(stage) + n * STRIDE + 8 * g, out = lds_address(stage) + r * STRIDE + 2 * c;
@@ -276,14 +280,14 @@ __device__ __forceinline__ void store_rounded(const f32x4 (&acc)[G::TM][G::TN], 
     if constexpr (STEPS == 1) {
       f32x4 o;
       asm volatile("ds_read_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(o) : "v"(out) : "memory");
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), to, at, 0, 0);
+      put(to, at, __builtin_bit_cast(u32x4, o), past);
     } else {
       f32x4 o[STEPS];
       read_part<STEPS, ROWS * STRIDE, 2 * ROWS * STRIDE, 3 * ROWS * STRIDE>(out, o);
 #pragma unroll
       for (int k = 0; k < STEPS; ++k) {
         const f32x4 x = o[k];
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), to, at + k * step, 0, 0);
+        put(to, at + k * step, __builtin_bit_cast(u32x4, x), past);
       }
     }
   }
@@ -327,19 +331,19 @@ __device__ __forceinline__ void store_part(const f32x4 (&acc)[G::TM][G::TN], con
 }
 
 // This wave's sums, rows row0 + 16 i .., columns col0 + 16 j .., to y; rows from `end` on and columns from N on are not there.
-// `whole`: rows of y, z and the residual suit store_whole.
+// `whole`: 0 where rows of y, z and the residual do not suit store_whole, 2 where y is not to be kept in the caches.
 template <int OUT, class G>
 __device__ __forceinline__ void store_epilogue(const f32x4 (&acc)[G::TM][G::TN], const fp4_epilogue& epi, int64_t bias_at, void* y,
                                                int64_t ldy, int row0, int end, int col0, int N, int lane, uint8_t* stage, int whole) {
   const int rows = min(end - row0, 16 * G::TM);
   if (rows <= 0 || col0 >= N) return;
-#define MX_WHOLE(RES, Z) store_whole<OUT, G, RES, Z>(acc, epi, bias_at, y, ldy, row0, rows, col0, lane, stage)
+#define MX_WHOLE(RES, Z) store_whole<OUT, G, RES, Z>(acc, epi, bias_at, y, ldy, row0, rows, col0, lane, stage, whole > 1)
   if (!whole || col0 + 16 * G::TN > N) {
     store_part<OUT, G>(acc, epi, bias_at, y, ldy, row0, rows, col0, N, lane, stage);
   } else if (!epi.residual) {
     if (epi.z) MX_WHOLE(0, true);
     else if constexpr (OUT == FP4_TYPE_F32) MX_WHOLE(0, false);
-    else store_rounded<OUT, G>(acc, epi, bias_at, y, ldy, row0, rows, col0, lane, stage);
+    else store_rounded<OUT, G>(acc, epi, bias_at, y, ldy, row0, rows, col0, lane, stage, whole > 1);
   } else if (epi.residual_type == FP4_TYPE_F32) {
     if (epi.z) MX_WHOLE(2, true);
     else MX_WHOLE(2, false);
@@ -536,6 +540,12 @@ static inline bool suits(const void* p, int64_t ld, int eb) { return !p || (fp4_
 template <class G, int OUT, Mode MODE>
 static int launch_product(Args p, int64_t tiles, hipStream_t st) {
   p.whole = suits(p.y, p.ldy, elem_bytes(OUT)) && suits(p.epi.residual, p.epi.ldr, elem_bytes(p.epi.residual_type)) && suits(p.epi.z, p.epi.ldz, 4);
+  // An output that the L2s cannot hold goes past them: kept, its lines would be written back in the next tiles' way, whose
+  // stores then wait for memory while the matrix core idles. 8192 x 14336 x 4096 with gelu 375 -> 330 us, weight gradients of
+  // 16 experts of 4096 x 2560 195 -> 150 us with their quantisation. Not beside a z, twice y's size: 622 -> 646 us for the
+  // training step of 8192 x 9728 x 2560.
+  const int64_t bytes = (int64_t)p.M * p.N * elem_bytes(OUT) * (MODE == DEPTH ? p.groups.E : 1);
+  if (p.whole && !p.epi.z && bytes > (32 << 20)) p.whole = 2;
   static Fp4LdsLimit limit;
   const int lds = G::LDS + (MODE == DENSE ? 0 : group_table_bytes(p.groups.E));
   limit.ensure(reinterpret_cast<const void*>(&product_kernel<G, OUT, MODE>), G::LDS + (MODE == DENSE ? 0 : group_table_bytes(MAX_GROUPS)));
