@@ -108,13 +108,14 @@ __global__ void __launch_bounds__(64 * W) quantize_grouped_kernel(Segments p) {
   float sum[4] = {0, 0, 0, 0};
   if constexpr (ACT != FP4_ACT_NONE) {
     // four rows of z at a time, the next four on their way meanwhile: all 32 do not fit the registers. Rows behind the last
-    // one are not read; a lane at the matrix's edge reads into the next row, which `in` drops.
+    // one are not read; a lane at the matrix's edge reads into the next row, which `in` drops. z is marked as not to be kept
+    // in the caches, where the operands made here will be read from (8192 x 9728: a step of 613 us takes 591).
     const auto zr = fp4::make_rsrc(p.z + (int64_t)from * p.ldz, (uint32_t)(min(last, 31) * (int)p.ldz + K) * 4);
     const bool in[4] = {col < K, col + 1 < K, col + 2 < K, col + 3 < K};
     u32x4 z[2][4];
     const auto ask = [&](int b) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) z[b & 1][i] = __builtin_amdgcn_raw_buffer_load_b128(zr, ((4 * b + i) * (int)p.ldz + col) * 4, 0, 0);
+      for (int i = 0; i < 4; ++i) z[b & 1][i] = __builtin_amdgcn_raw_buffer_load_b128(zr, ((4 * b + i) * (int)p.ldz + col) * 4, 0, 2);
     };
     ask(0);
 #pragma unroll
