@@ -357,10 +357,10 @@ __device__ __forceinline__ void store_epilogue(const f32x4 (&acc)[G::TM][G::TN],
 // Rows of no group: the residual, or zero.
 template <int OUT>
 __device__ __forceinline__ void fill_row(const fp4_epilogue& epi, void* y, int64_t ldy, int64_t row, int N, int thread, int threads) {
-  for (int c = thread; c < N; c += threads) {
-    float f[1] = {0};
-    if (epi.residual) values_of(epi.residual_type, load_raw<1>(epi.residual_type, epi.residual, row * epi.ldr + c, 1), f);
-    store_values<OUT>(y, row * ldy + c, f, 1);
+  for (int c = 8 * thread; c < N; c += 8 * threads) {
+    float f[8] = {};
+    if (epi.residual) values_of(epi.residual_type, load_raw<8>(epi.residual_type, epi.residual, row * epi.ldr + c, N - c), f);
+    store_values<OUT>(y, row * ldy + c, f, N - c);
   }
 }
 
