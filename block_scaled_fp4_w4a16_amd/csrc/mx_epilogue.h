@@ -115,6 +115,21 @@ __device__ __forceinline__ void values_of(int type, const Raw<W>& r, float (&f)[
   }
 }
 
+// P pieces of W values, every one there, `step` elements apart: all are asked for before the first is waited for.
+template <int P, int W>
+__device__ __forceinline__ void load_pieces(int type, const void* p, int64_t at, int step, float (&f)[P][W]) {
+  Raw<W> r[P] = {};
+  if (type == FP4_TYPE_F32) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) __builtin_memcpy(r[i].v, static_cast<const uint8_t*>(p) + (at + i * step) * 4, 4 * W);
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) __builtin_memcpy(r[i].v, static_cast<const uint8_t*>(p) + (at + i * step) * 2, 2 * W);
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) values_of(type, r[i], f[i]);
+}
+
 // W values, n of them, to element `at` of y.
 template <int OUT, int W>
 __device__ __forceinline__ void store_values(void* y, int64_t at, const float (&f)[W], int n) {

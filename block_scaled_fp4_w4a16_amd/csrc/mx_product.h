@@ -172,13 +172,8 @@ __device__ __forceinline__ void store_whole(const f32x4 (&acc)[G::TM][G::TN], co
   if constexpr (Z) keep = descriptor(epi.z, epi.ldz, 4);
   const int res_type = RES == 2 ? FP4_TYPE_F32 : epi.residual_type == FP4_TYPE_BF16 ? FP4_TYPE_BF16 : FP4_TYPE_F16;
 
-  float bias[P::SPLIT][W];
-#pragma unroll
-  for (int h = 0; h < P::SPLIT; ++h) {
-#pragma unroll
-    for (int i = 0; i < W; ++i) bias[h][i] = 0;
-    if (epi.bias) values_of(epi.bias_type, load_raw<W>(epi.bias_type, epi.bias, bias_at + col0 + h * P::COLS + c, W), bias[h]);
-  }
+  float bias[P::SPLIT][W] = {};
+  if (epi.bias) load_pieces(epi.bias_type, epi.bias, bias_at + col0 + c, P::COLS, bias);
   Raw<W> ahead[U][P::STEPS];
   if constexpr (RES != 0)
 #pragma unroll
@@ -247,13 +242,8 @@ __device__ __forceinline__ void store_rounded(const f32x4 (&acc)[G::TM][G::TN], 
   const int n = lane & 15, g = lane >> 4, r = lane / PER, c = lane % PER * 8;
   const uint32_t in = lds_address(stage) + n * STRIDE + 8 * g, out = lds_address(stage) + r * STRIDE + 2 * c;
   const auto to = fp4::make_rsrc(static_cast<uint8_t*>(y) + (row0 * ldy + col0) * 2, (uint32_t)(((rows - 1) * (int)ldy + COLS) * 2));
-  float bias[TN][4];
-#pragma unroll
-  for (int j = 0; j < TN; ++j) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) bias[j][e] = 0;
-    if (epi.bias) values_of(epi.bias_type, load_raw<4>(epi.bias_type, epi.bias, bias_at + col0 + 16 * j + 4 * g, 4), bias[j]);
-  }
+  float bias[TN][4] = {};
+  if (epi.bias) load_pieces(epi.bias_type, epi.bias, bias_at + col0 + 4 * g, 16, bias);
   const int all = min(G::TM, (rows + 15) / 16);
 #pragma unroll 1
   for (int i = 0; i < all; ++i) {
