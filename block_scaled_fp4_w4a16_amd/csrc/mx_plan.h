@@ -87,18 +87,18 @@ inline bool fused(int64_t M, int64_t N, int64_t K) {
   return M <= 16 && (N + 15) / 16 * stages_of(K) * (M + 3) <= 32768;
 }
 
-// The figures of tiles with an epilogue: what it adds to each round, as measured at 8192 x 14336 x 4096 and 8192 x 9728 x 2560. The
-// matrix core idles through it in tiles of 256, one of which fits a unit; tiles of 128 cover each other's. So gelu onto a
-// residual at 8192 x 9728 x 2560 takes 226 us in tiles of 256 and 203 in tiles of 128, a bias alone 124 and 130; at
-// 14336 x 4096 382 and 399, 270 and 327.
+// The figures of tiles with an epilogue: what it adds to each round, as measured at 8192 x 14336 x 4096 and 8192 x 9728 x 2560 with
+// 16-bit outputs. The matrix core idles through it in tiles of 256, one of which fits a unit; tiles of 128 cover each other's. So
+// gelu onto a residual at 8192 x 9728 x 2560 takes 211 us in tiles of 256 and 173 in tiles of 128, a bias alone 127 and 126; at
+// 14336 x 4096 369 and 372, 251 and 285.
 struct EpilogueCosts {
   TileCost of[3];
 };
 inline EpilogueCosts epilogue_costs(bool erf, bool other_activation, bool residual, bool z) {
   EpilogueCosts e{{TILE_COSTS[0], TILE_COSTS[1], TILE_COSTS[2]}};
   const double more[3] = {0.3 + (erf ? 0.8 : other_activation ? 0.3 : 0) + (residual ? 1 : 0) + (z ? 2 : 0),
-                          1.5 + (erf ? 2.5 : other_activation ? 0.7 : 0) + (residual ? 4.5 : 0) + (z ? 9 : 0),
-                          5.0 + (erf ? 8 : other_activation ? 3 : 0) + (residual ? 9 : 0) + (z ? 13 : 0)};
+                          0.2 + (erf ? 2.5 : other_activation ? 0.8 : 0) + (residual ? 3.5 : 0) + (z ? 9 : 0),
+                          3.7 + (erf ? 8 : other_activation ? 2.4 : 0) + (residual ? 9.7 : 0) + (z ? 13 : 0)};
   for (int i = 0; i < 3; ++i) e.of[i].launch += more[i], e.of[i].round += more[i];
   return e;
 }
