@@ -105,17 +105,18 @@ inline EpilogueCosts epilogue_costs(bool erf, bool other_activation, bool residu
 
 // Tiles of rows in groups: 64, 64 x 128 (WIDE; few rows of many groups, bound by the weights' bytes), 128 and 256 square. All but
 // those of 64 are taken as streams, so that a round costs its stages and its way out; those of 64, which have more stages on
-// their way, are for what leaves units idle (200 rows in 8 groups, 1024 columns, K = 2560: 7.8 us, in 64 x 128 12.9).
+// their way, are for what leaves units idle (200 rows in 8 groups, 1024 columns, K = 2560: 6.6 us, in 64 x 128 8.7).
 constexpr int WIDE = 96;
 inline int tile_rows(int tile) { return tile == WIDE ? 64 : tile; }
 inline int tile_columns(int tile) { return tile == WIDE ? 128 : tile; }
-constexpr TileCost GROUPED_COSTS[] = {{64, 5, 4, 0.27, 0.5}, {WIDE, 6.3, 2.3, 0.6, 0.95}, {128, 9, 5, 0.8, 1.25}, {256, 17, 13, 1.75, 0}};
+constexpr TileCost GROUPED_COSTS[] = {{64, 5, 4, 0.27, 0.5}, {WIDE, 6.3, 2.3, 0.6, 0.95}, {128, 7, 4.4, 0.75, 1.1}, {256, 15, 11, 1.75, 0}};
 constexpr TileCost GRADIENT_COSTS[] = {{128, 7.5, 3.5, 0.8, 1.25}, {256, 11, 7, 1.75, 0}};
 
 // The tiles of a product of T rows in E groups, whose sizes only the device knows, with N columns and depth K: the cheapest
 // by those figures for groups of equal size, each of which ends inside a tile. 0: rows_grouped_kernel, for up to 16 rows.
-// Measured in tiles of 64 x 128, 128 and 256, in us: 512 rows in 64 groups, 2560 columns, K = 1024: 19.6, 23, 36; 4000 in 32, 2560,
-// 2560: 39.5, 36, 61; 8192 in 16, 4096, 2560: 98, 82, 89; 16384 in 8, 14336, 4096: 1027, 775, 593.
+// Measured in tiles of 64 x 128, 128 and 256, in us: 512 rows in 64 groups, 2560 columns, K = 1024: 18, 20, 33; 4000 in 32, 2560,
+// 2560: 38, 33, 51; 8192 in 16, 4096, 2560: 80, 66, 75; 4096 in 8, 14336, 4096: 216, 176, 186; 16384 in 8: 828, 639, 568. Where the
+// weights' bytes set the time of more than one, their own figures decide: 2000 in 64, 1024, 2560: 17.9, 19.5, 28.1, in tiles of 64 20.2.
 inline int grouped_tile(int64_t T, int64_t N, int64_t K, int64_t E, int cus) {
   if (T <= 16) return 0;
   const double some = E < T ? E : T, each = T / some, least = 3.5 + some * N * K * (17 / 32.) / 5e6;
@@ -124,14 +125,14 @@ inline int grouped_tile(int64_t T, int64_t N, int64_t K, int64_t E, int cus) {
   for (const TileCost& c : GROUPED_COSTS) {
     const double down = each / tile_rows(c.tile) + 0.5, rows = some * (down > 1 ? down : 1);
     double us = tiles_us(c, (int64_t)(rows * ((N + tile_columns(c.tile) - 1) / tile_columns(c.tile))), (stages_of(K) + 1) & ~1, cus);
-    if (us < least) us = least;
+    if (us < least) us = least + 0.01 * us;
     if (us < best) best = us, tile = c.tile;
   }
   return tile;
 }
 
-// The tiles of E products of M x N outputs that contract T rows between them. 8192 rows, 16 of 4096 x 2560: 150 us in tiles of
-// 128, 134 in tiles of 256; 200 rows, 8 of 1024 x 2560 in FP32: 24 and 35.
+// The tiles of E products of M x N outputs that contract T rows between them. With the gradient's quantisation, in tiles of 128 and
+// 256: 8192 rows, 16 of 4096 x 2560: 154 and 150 us; 16384, 2 of 4096 x 4096: 197 and 169; 200 rows, 8 of 1024 x 2560 in FP32: 29 and 42.
 inline int gradient_tile(int64_t T, int64_t M, int64_t N, int64_t E, int cus) {
   int tile = 0;
   double best = 1e30;
