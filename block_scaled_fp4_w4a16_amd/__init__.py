@@ -90,6 +90,8 @@ _SIGS = {
     "w4a4_linear_workspace_bytes": (_i64, [_i64, _i64, _i64]),
     "w4a4_matmul_epilogue": (_c, [_c, _i64, _i64, _i64, _mx, _mx, _epi, _p, _i64, _p, ctypes.c_size_t, _p]),
     "w4a4_linear_epilogue": (_c, [_c, _c, _i64, _i64, _i64, _p, _i64, _mx, _epi, _p, _i64, _p, ctypes.c_size_t, _p]),
+    "w4a4_matmul_epilogue_workspace_bytes": (_i64, [_i64, _i64, _i64, _epi]),
+    "w4a4_linear_epilogue_workspace_bytes": (_i64, [_i64, _i64, _i64, _epi]),
     "w4a4_grouped_matmul": (_c, [_c, _i64, _i64, _i64, _groups, _mx, _mx, _epi, _c, _p, _i64, _p]),
     "w4a4_grouped_linear": (_c, [_c, _c, _i64, _i64, _i64, _groups, _p, _i64, _mx, _epi, _c, _p, _i64, _p, ctypes.c_size_t, _p]),
     "w4a4_grouped_linear_workspace_bytes": (_i64, [_i64, _i64, _i64, _i64]),
@@ -476,12 +478,12 @@ def _mx_workspace_bytes(name, M, N, K, device) -> int:
 
 
 def w4a4_matmul_workspace_bytes(M, N, K, device=None) -> int:
-    """Workspace bytes w4a4_matmul can use for this shape on `device` (default: the current one)."""
+    """Workspace bytes w4a4_matmul can use for this shape, whatever follows the product, on `device` (default: the current one)."""
     return _mx_workspace_bytes("w4a4_matmul_workspace_bytes", M, N, K, device)
 
 
 def w4a4_linear_workspace_bytes(M, N, K, device=None) -> int:
-    """Workspace bytes of w4a4_linear for this shape on `device` (default: the current one)."""
+    """Workspace bytes of w4a4_linear for this shape, whatever follows the product, on `device` (default: the current one)."""
     return _mx_workspace_bytes("w4a4_linear_workspace_bytes", M, N, K, device)
 
 

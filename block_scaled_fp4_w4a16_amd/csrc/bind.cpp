@@ -285,7 +285,7 @@ void product_into(int64_t M, int64_t N, int64_t K, const fp4_mx& a, const fp4_mx
   const int type = dense_type(y, "y");
   const int64_t ldy = rows_of(y, M, N, "y");
   c10::DeviceGuard guard(d);
-  const int64_t need = ws ? 0 : w4a4_matmul_workspace_bytes(M, N, K);
+  const int64_t need = ws ? 0 : w4a4_matmul_epilogue_workspace_bytes(M, N, K, after);
   check(need, "w4a4_matmul");
   const Workspace w = workspace_of(ws, need, d);
   if (after)
@@ -316,7 +316,7 @@ void linear_into(int64_t M, int64_t N, int64_t K, const Tensor& x, const Operand
   const int64_t ldx = rows_of(x, M, K, "x"), ldy = rows_of(y, M, N, "y");
   const fp4_mx b = operand(B.codes, B.scales, N, K, "B");
   c10::DeviceGuard guard(d);
-  const int64_t need = ws ? 0 : w4a4_linear_workspace_bytes(M, N, K);
+  const int64_t need = ws ? 0 : w4a4_linear_epilogue_workspace_bytes(M, N, K, after);
   check(need, "w4a4_linear");
   const Workspace w = workspace_of(ws, need, d);
   if (after)

@@ -272,11 +272,6 @@ int launch_planes(int tile, int parts, int per, int64_t ldp, int M, int N, int K
 
 using namespace mx;
 
-extern "C" int64_t w4a4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (int rc = check_product(FP4_TYPE_F32, M, N, K)) return rc;
-  return M == 0 ? 0 : plane_bytes(plan_of(M, N, K, fp4_device_cus()), M);
-}
-
 extern "C" int w4a4_matmul(int out_type, int64_t M, int64_t N, int64_t K, const fp4_mx* a, const fp4_mx* b, void* y,
                            int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
   if (int rc = check_product(out_type, M, N, K)) return rc;
@@ -287,13 +282,6 @@ extern "C" int w4a4_matmul(int out_type, int64_t M, int64_t N, int64_t K, const 
   if (workspace && !fp4_aligned(workspace, 16)) return FP4_ERR_ALIGN;
   return run_product(plan_of(M, N, K, fp4_device_cus()), out_type, M, N, K, *a, *b, y, ldy, workspace, workspace_bytes,
                      static_cast<hipStream_t>(stream));
-}
-
-extern "C" int64_t w4a4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (int rc = check_product(FP4_TYPE_F32, M, N, K)) return rc;
-  if (M == 0 || fused(M, N, K)) return 0;
-  const LinearSpace sp = linear_space(plan_of(M, N, K, fp4_device_cus()), M, K);
-  return sp.q + sp.s + sp.planes;
 }
 
 extern "C" int w4a4_linear(int x_type, int out_type, int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx,

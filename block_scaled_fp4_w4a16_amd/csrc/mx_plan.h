@@ -40,7 +40,11 @@ inline double tiles_us(const TileCost& c, int64_t work, int stages, int cus) {
 // K = 9728: tiles of 64 take 13.1 us, of 128 28.9 us; 64 x 2560, K = 9728: 12.8 us, in 4 parts 9.3 us.
 // Where the last round of tiles of 256 would be a small one (split), the columns that fill whole rounds are one product and
 // the others a second in tiles that fill the device.
-inline Plan plan_of(int64_t M, int64_t N, int64_t K, int cus, bool split = true, const TileCost* costs = TILE_COSTS) {
+// `costs`: what an epilogue makes of the tiles' figures. Where K is in parts the second kernel has it, which is taken to cost what it
+// does in tiles of 64, so that it has no say in how many parts there are (20 x 635, K = 8192 with a bias: in 8 parts 8.5 us, in 16
+// 10.0, whole 10.9). `room`: bytes that the planes may take.
+inline Plan plan_of(int64_t M, int64_t N, int64_t K, int cus, bool split = true, const TileCost* costs = TILE_COSTS,
+                    int64_t room = INT64_MAX) {
   Plan p{};
   p.ldp = (N + 3) / 4 * 4;
   const int stages = stages_of(K);
@@ -53,22 +57,22 @@ inline Plan plan_of(int64_t M, int64_t N, int64_t K, int cus, bool split = true,
   if (M <= 16) p.us = 1.8 + (double)((N + 15) / 16) * stages * (0.00034 + 0.00001 * M);
   const double least = 3.5 + N * K * (17 / 32.) / 5e6;  // the weights' bytes at 5 TB/s
   for (int i = 0; i < 3; ++i) {
-    const TileCost& c = costs[i];
-    const int64_t tiles = ((M + c.tile - 1) / c.tile) * ((N + c.tile - 1) / c.tile);
+    const int64_t tile = costs[i].tile, tiles = ((M + tile - 1) / tile) * ((N + tile - 1) / tile);
     for (int want = 1; want <= 16; want *= 2) {
       const int per = ((stages + want - 1) / want + 1) & ~1, parts = (stages + per - 1) / per;
-      if (want > 1 && (c.tile == 256 || parts != want || tiles * parts > cus)) break;
-      double us = tiles_us(c, tiles * parts, per, cus);
+      if (want > 1 && (tile == 256 || parts != want || tiles * parts > cus || parts * M * p.ldp * 4 > room)) break;
+      double us = tiles_us(parts > 1 ? TILE_COSTS[i] : costs[i], tiles * parts, per, cus);
       if (us < least) us = least;
-      if (parts > 1) us += 2.5 + parts * M * p.ldp * 4 / 1.2e6;
-      if (us < p.us) p.us = us, p.tile = c.tile, p.parts = parts, p.per = per;
+      if (parts > 1) us += 2.5 + parts * M * p.ldp * 4 / 1.2e6 + (costs[0].launch - TILE_COSTS[0].launch);
+      if (us < p.us) p.us = us, p.tile = (int)tile, p.parts = parts, p.per = per;
     }
   }
   if (split) {
     const TileCost& c = costs[2];
     const int64_t down = (M + 255) / 256, across = (N + 255) / 256, fit = down * across / cus * cus / down;
     if (fit > 0 && fit < across) {
-      const Plan rest = plan_of(M, N - fit * 256, K, cus, false, costs);
+      // the second product has no planes; a product without an epilogue whose second one would want them stays one
+      const Plan rest = plan_of(M, N - fit * 256, K, cus, false, costs, costs == TILE_COSTS ? room : 0);
       const double us = tiles_us(c, down * fit, (stages + 1) & ~1, cus) + rest.us;
       if (rest.parts == 1 && us < 0.95 * p.us)
         p.us = us, p.tile = 256, p.parts = 1, p.per = (stages + 1) & ~1, p.first_n = fit * 256;

@@ -371,7 +371,10 @@ int fp4_dequant_mxfp4(int type, int64_t M, int64_t K, const fp4_mx* a, void* out
 int w4a4_matmul(int out_type, int64_t M, int64_t N, int64_t K, const fp4_mx* a, const fp4_mx* b, void* y,
                 int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes w4a4_matmul can use for this shape on the current device, or a negative status. */
+/*
+ * Workspace bytes w4a4_matmul, and w4a4_matmul_epilogue with any epilogue, can use for this shape on the current device, or a
+ * negative status. w4a4_matmul_epilogue_workspace_bytes() says it of one call.
+ */
 int64_t w4a4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /*
@@ -384,7 +387,10 @@ int64_t w4a4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int w4a4_linear(int x_type, int out_type, int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx,
                 const fp4_mx* b, void* y, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of w4a4_linear for this shape on the current device (0: it takes none), or a negative status. */
+/*
+ * Workspace bytes of w4a4_linear, and of w4a4_linear_epilogue with any epilogue, for this shape on the current device (0: they
+ * take none), or a negative status. w4a4_linear_epilogue_workspace_bytes() says it of one call.
+ */
 int64_t w4a4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /*
@@ -420,9 +426,11 @@ typedef struct fp4_epilogue {
 } fp4_epilogue;
 
 /*
- * w4a4_matmul and w4a4_linear with an epilogue: the same operands, kernels and workspaces (w4a4_matmul_workspace_bytes(),
- * w4a4_linear_workspace_bytes()). Errors as theirs, and for the epilogue FP4_ERR_ARG (NULL, unknown activation or type),
- * FP4_ERR_SHAPE (a stride below N), FP4_ERR_ALIGN, FP4_ERR_UNSUPPORTED (a stride too large).
+ * w4a4_matmul and w4a4_linear with an epilogue: the same operands, kernels and workspaces. With less workspace than the two queries
+ * below name, K is split into as many parts as fit, or not at all. Errors as theirs, and for the epilogue FP4_ERR_ARG (NULL,
+ * unknown activation or type), FP4_ERR_SHAPE (a stride below N), FP4_ERR_ALIGN, FP4_ERR_UNSUPPORTED (a stride too large).
+ * The queries: workspace bytes for this shape and epilogue on the current device, or a negative status; of the epilogue they look
+ * at which pointers are NULL, types, strides, alignments and the activation. NULL: those of the call without an epilogue.
  */
 int w4a4_matmul_epilogue(int out_type, int64_t M, int64_t N, int64_t K, const fp4_mx* a, const fp4_mx* b,
                          const fp4_epilogue* epilogue, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
@@ -430,6 +438,8 @@ int w4a4_matmul_epilogue(int out_type, int64_t M, int64_t N, int64_t K, const fp
 int w4a4_linear_epilogue(int x_type, int out_type, int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx,
                          const fp4_mx* b, const fp4_epilogue* epilogue, void* y, int64_t ldy, void* workspace,
                          size_t workspace_bytes, void* stream);
+int64_t w4a4_matmul_epilogue_workspace_bytes(int64_t M, int64_t N, int64_t K, const fp4_epilogue* epilogue);
+int64_t w4a4_linear_epilogue_workspace_bytes(int64_t M, int64_t N, int64_t K, const fp4_epilogue* epilogue);
 
 /*
  * Rows in groups, one group per expert: group e's rows are [offsets[e], offsets[e + 1]), e = 0 .. count - 1. The count + 1
