@@ -374,14 +374,13 @@ __global__ void __launch_bounds__(G::THREADS, G::LDS > 80 * 1024 ? G::WAVES / 4 
   w.src.ldqa = (int)p.a.ldq, w.src.ldqb = (int)p.b.ldq, w.src.ldsa = (int)p.a.lds, w.src.ldsb = (int)p.b.lds;
 
   int* const start = reinterpret_cast<int*>(lds + G::LDS);
-  int* const units = start + p.groups.E + 1;
   int total = p.tiles_m * p.tiles_n;
   if constexpr (MODE != DENSE) {
-    if (w.wave == 0) read_groups<MODE == ROWS ? BM : UNIT>(p.groups, MODE == ROWS ? p.M : p.K, start, units, w.lane);
+    if (w.wave == 0) start[p.groups.E + 1] = read_groups<MODE == ROWS ? BM : UNIT>(p.groups, MODE == ROWS ? p.M : p.K, start, nullptr, w.lane);
     __syncthreads();
     if constexpr (MODE == DEPTH) total *= p.groups.E;
     if constexpr (MODE == ROWS) {
-      total = uniform(units[p.groups.E]) * p.tiles_n;
+      total = uniform(start[p.groups.E + 1]) * p.tiles_n;
       if (p.fill) {
         const int first = uniform(start[0]), last = uniform(start[p.groups.E]);
         for (int r = blockIdx.x; r < first + p.M - last; r += gridDim.x)
@@ -422,16 +421,16 @@ __global__ void __launch_bounds__(G::THREADS, G::LDS > 80 * 1024 ? G::WAVES / 4 
     j.e = j.from = 0, j.end = p.M, j.nb = (int)blocks_of(p.K);
     int first = 0, tiles_m = p.tiles_m;
     if constexpr (MODE == ROWS) {
-      j.e = group_of(units, p.groups.E, t / p.tiles_n, w.lane);
-      const int before = uniform(units[j.e]);
-      t -= before * p.tiles_n;
-      tiles_m = uniform(units[j.e + 1]) - before;
+      const Found f = find_group<BM>(start, p.groups.E, t / p.tiles_n, w.lane);
+      j.e = f.e;
+      t -= f.before * p.tiles_n;
       first = uniform(start[j.e]), j.end = uniform(start[j.e + 1]);
+      tiles_m = (j.end - first + BM - 1) / BM;
     } else if constexpr (MODE == DEPTH) {
       j.e = t / whole;
       t -= j.e * whole;
       j.nb = (uniform(start[j.e + 1]) - uniform(start[j.e]) + BLOCK - 1) / BLOCK;
-      j.from = uniform(units[j.e]) * (UNIT / BLOCK);
+      j.from = units_before<UNIT>(start, j.e, w.lane) * (UNIT / BLOCK);
     }
     walk(t, tiles_m, p.tiles_n, tm, tn);
     j.m0 = first + tm * BM, j.n0 = tn * BN;
@@ -552,6 +551,9 @@ using Tile64 = Tile<64, 64, 2, 2, 4, 2>;
 using TileWide = Tile<64, 128, 2, 2, 2, 1>;
 static_assert(Tile256::STAGE >= 16 * (64 * 4 + 16) && Tile128::STAGE >= 16 * (32 * 4 + 16), "a wave's staging rows of FP32 sums");
 static_assert(Tile256::LDS + group_table_bytes(MAX_GROUPS) <= 160 * 1024, "");
+static_assert(Tile128::LDS + group_table_bytes(MAX_GROUPS) <= 80 * 1024 && Tile64::LDS + group_table_bytes(MAX_GROUPS) <= 80 * 1024 &&
+                  TileWide::LDS + group_table_bytes(MAX_GROUPS) <= 80 * 1024,
+              "two workgroups to a compute unit (PER_UNIT)");
 
 template <int OUT, Mode MODE>
 static int launch_tile(int tile, const Args& p, int64_t tiles, hipStream_t st) {

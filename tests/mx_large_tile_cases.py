@@ -18,3 +18,6 @@ GROUPED_EPILOGUES = [(None, "bf16", None, "bf16"), ("relu", "bf16", None, "f16")
 # rows of each group, with one to five stages of 256 of them in every order; (in front, behind); rows and columns of a gradient
 GRADIENTS = [((1100, 0, 513, 1, 257, 700, 255), (0, 0), 4096, 2560), ((255, 700, 257, 1, 1024, 513, 0, 1100), (3, 40), 4098, 2570),
              ((1, 513, 512, 1100, 256, 0, 700), (0, 9), 4095, 2559)]
+# rows, columns, depth, groups of a product in tiles of 128; rows, rows and columns of a gradient, groups
+MANY_GROUPS = [(40_000, 1024, 1024, 384), (40_000, 1026, 1000, 512), (30_001, 1500, 544, 449)]
+MANY_GRADIENTS = [(3000, 130, 136, 384), (2600, 128, 264, 512)]

@@ -166,3 +166,47 @@ def test_layer_of_experts_keeps_its_sums():
         assert torch.equal(dwi, dw[i])
         # values of at most 1.13 |g|; both sums take up to 40 additions in FP32 and are rounded at the end
         assert ((dbi - db[i]).abs() <= 2 * 42 * 2.0 ** -24 * 1.13 * g[lo:hi].double().abs().sum(0)).all()
+
+
+def uneven(t, e, *key, front=0, behind=0):
+    """Bounds of e groups, many of them empty or of one row."""
+    r = np.random.default_rng([t, e, *key])
+    share = np.exp2(r.integers(0, 7, e)) * (r.random(e) < 0.7)
+    share[0], share[-1] = 0, 1                                             # the last group has rows, the first has none
+    cuts = np.floor(np.cumsum(share) / share.sum() * (t - front - behind) + 1e-9).astype(np.int64)
+    return np.concatenate([[0], cuts]) + front
+
+
+@pytest.mark.parametrize("t,n,k,e", cases.MANY_GROUPS)
+def test_many_groups(t, n, k, e):
+    off = uneven(t, e, 20, front=2, behind=9)
+    offsets = torch.from_numpy(off).cuda()
+    a, w, bias = operand(t, k, 21), operand(e * n, k, 22, low=120), dense(e, n, torch.float32, 23)
+    y = w.grouped_matmul(a, offsets, out_dtype=torch.bfloat16, bias=bias, activation="silu")
+    assert not y[:2].any() and not y[-9:].any()
+    r = np.random.default_rng([t, 24])
+    some = [i for i in range(e) if off[i] < off[i + 1]]
+    assert some[-1] == e - 1 and len(some) > e // 2
+    for i in sorted({*r.choice(some, 25, replace=False), some[0], some[-1], *[j for j in some if 60 < j % 64 or j % 64 < 2][:12]}):
+        rows = np.unique([off[i], off[i + 1] - 1, r.integers(off[i], off[i + 1])])
+        vb = fp4.MXTensor(w.codes[i * n:(i + 1) * n], w.scales[i * n:(i + 1) * n], n, k).dequant().double()
+        at = torch.from_numpy(rows).cuda()
+        va = fp4.MXTensor(a.codes[at], a.scales[at], len(rows), k)
+        va = fp4.MXTensor.from_canonical(va.codes, va.scales, k).dequant().double()
+        z, ez = ref.with_bias(*sums(va, vb, k), f64(bias[i]))
+        ref.check(y[at], *ref.out(z, ez, "silu", None, y.dtype), label=f"{t} {e} {i}")
+
+
+@pytest.mark.parametrize("t,m,n,e", cases.MANY_GRADIENTS)
+def test_weight_gradients_of_many_groups(t, m, n, e):
+    off = uneven(t, e, 25, behind=5)
+    offsets = torch.from_numpy(off).cuda()
+    x, g = dense(t, n, torch.bfloat16, 26), dense(t, m, torch.bfloat16, 27)
+    w = torch.zeros(e, m, n, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    (dw,) = torch.autograd.grad(fp4.mx_grouped_linear(x, w, offsets), w, g)
+    for i, (lo, hi) in enumerate(zip(off, off[1:])):
+        if lo == hi:
+            assert not dw[i].any()
+            continue
+        want, tol = ref.product(ref.values(g[lo:hi].T), ref.values(x[lo:hi].T), hi - lo)
+        ref.check(dw[i], want, ref.rounded(want, tol, dw.dtype), f"{t} {e} {i}")

@@ -52,3 +52,10 @@ def test_every_case_runs_tiles_of_256(rules):
     # every way out: each activation without a residual, rounded in the tile, and with the sums kept
     for kept in (False, True):
         assert {e[0] for e in cases.EPILOGUES if e[3] == kept and e[2] is None} == {None, "relu", "silu", "gelu", "gelu_tanh"}
+
+
+def test_cases_of_many_groups_run_tiles_of_128(rules):
+    for sizes in cases.MANY_GROUPS:
+        assert rules.grouped(*(ctypes.c_int64(v) for v in sizes)) == 128, sizes
+    for sizes in cases.MANY_GRADIENTS:
+        assert rules.gradient(*(ctypes.c_int64(v) for v in sizes)) == 128, sizes
