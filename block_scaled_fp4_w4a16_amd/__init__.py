@@ -489,8 +489,8 @@ def w4a4_linear_workspace_bytes(M, N, K, device=None) -> int:
 
 def w4a4_matmul(M, N, K, aq, a_s, bq, bs, y, stream=None, workspace=None, bias=None, activation=None, residual=None):
     """y [M, N] (float32, bfloat16 or float16; rows may be strided) = f(A B^T + bias) + residual of two MXFP4 operands of depth
-    K, rounded once. bias [N], residual [M, N] (float32, bfloat16 or float16; it may be y itself) and the activation f, None,
-    "relu", "silu", "gelu" or "gelu_tanh", are each left out by default.
+    K, rounded once. bias [N], residual [M, N] (float32, bfloat16 or float16; it may be y itself, but shares no other memory with
+    it) and the activation f, None, "relu", "silu", "gelu" or "gelu_tanh", are each left out by default.
     `workspace`: a uint8 CUDA tensor, by default one of the size the library asks for, allocated here."""
     _native.matmul(M, N, K, aq, a_s, bq, bs, y, stream, workspace, bias, activation, residual)
 

@@ -2,6 +2,7 @@
 // the C entry points, and the trainable layer's autograd node. A decode-sized product runs for a few microseconds;
 // the same checks written in Python took 23 to 30 microseconds a call.
 #include <ATen/ATen.h>
+#include <ATen/MemoryOverlap.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/hip/HIPStream.h>
@@ -170,6 +171,21 @@ Tensor bias_of(const Tensor& b, int64_t groups, int64_t N) {
   return b.resolve_neg().contiguous();
 }
 
+// Whether two M x N matrices with contiguous rows share memory: by their places where they have the same row stride and element
+// size, else as far as torch can tell (it cannot of rows with gaps).
+bool share_memory(const Tensor& a, const Tensor& b, int64_t M, int64_t N, int64_t lda, int64_t ldb) {
+  if (M < 1 || N < 1) return false;
+  const int64_t eb = a.element_size();
+  if (lda != ldb || eb != (int64_t)b.element_size()) {
+    const auto s = at::get_overlap_status(a, b);
+    return s == at::MemOverlapStatus::Full || s == at::MemOverlapStatus::Partial;
+  }
+  // b lies `rows` rows and `at` bytes behind a, 0 <= at < a row's stride
+  const int64_t row = lda * eb, far = (int64_t)b.data_ptr() - (int64_t)a.data_ptr();
+  const int64_t rows = far >= 0 ? far / row : -((-far + row - 1) / row), at = far - rows * row;
+  return (at < N * eb && std::abs(rows) < M) || (at + N * eb > row && std::abs(rows + 1) < M);
+}
+
 // `e` as the library takes it, for y [M, N]; `bias` receives what the bias's pointer points to.
 fp4_epilogue native(const Epilogue& e, const Tensor& y, int64_t M, int64_t N, int64_t groups, c10::Device d, Tensor& bias) {
   fp4_epilogue n{};
@@ -185,8 +201,11 @@ fp4_epilogue native(const Epilogue& e, const Tensor& y, int64_t M, int64_t N, in
     n.residual_type = dense_type(r, "residual");
     n.ldr = rows_of(r, M, N, "residual");
     n.residual = r.data_ptr();
-    if (M > 0 && r.data_ptr() == y.data_ptr() && (r.scalar_type() != y.scalar_type() || n.ldr != rows_of(y, M, N, "y")))
+    const int64_t ldy = rows_of(y, M, N, "y");
+    const bool same = r.data_ptr() == y.data_ptr();
+    if (M > 0 && same && (r.scalar_type() != y.scalar_type() || n.ldr != ldy))
       value_error("a residual that is the output has to be so in type and strides too");
+    if (!same && share_memory(r, y, M, N, n.ldr, ldy)) value_error("the residual and the output share a part of their memory: one would change the other");
   }
   return n;
 }

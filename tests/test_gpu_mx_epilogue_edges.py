@@ -197,3 +197,29 @@ def test_the_same_rows_twice():
     z, ez = ref.with_bias(*ref.product(ref.values(x[rows]), ref.values(w[1]), K), f64(b[1]))
     ref.check(y, *ref.out(z, ez, "gelu", None, torch.float32))
     assert torch.equal(y[0], y[40]) and np.unique(f64(y)[[0, 1, 2, 8, *range(40, 70)]], axis=0).shape[0] == 1
+
+
+def test_a_residual_that_overlaps_the_output_is_refused():
+    """The same memory at the same place is added to; any other overlap would have one tile read what another wrote."""
+    x, w, b, _ = (v.detach() for v in leaves(24))
+    d, q, off = fp4.MXTensor.quantize(w[0]), fp4.MXTensor.quantize(w), torch.tensor(OFF, device="cuda")
+    bad, good = [], []
+    flat = torch.zeros((M + 2) * N + 8, device="cuda")
+    at = lambda start: flat[start:start + M * N].view(M, N)  # noqa: E731
+    bad += [(at(N), at(0)), (at(0), at(N)), (at(0), at(1)), (at(3), at(0)), (at(0), at(2 * N))]
+    wide = torch.zeros(M + 1, 3 * N, device="cuda")
+    col = lambda start, row=0: wide[row:row + M, start:start + N]  # noqa: E731
+    bad += [(col(0), col(N - 1)), (col(N), col(1)), (col(5), col(5, 1)), (col(2 * N, 0), col(2 * N - 3, 1)), (col(5, 1), col(9))]
+    good += [(col(0), col(N)), (col(2 * N), col(N)), (col(0, 1), col(2 * N)), (col(2 * N), col(0, 1)), (col(7), col(7))]
+    half = torch.zeros(4 * M * N, dtype=torch.bfloat16, device="cuda")
+    bad += [(half[:2 * M * N].view(torch.float32).view(M, N), half[M * N:2 * M * N].view(M, N))]
+    good += [(half[:2 * M * N].view(torch.float32).view(M, N), half[2 * M * N:3 * M * N].view(M, N)), (at(0), at(0))]
+    for y, r in bad:
+        for call in (lambda: d.matmul(x, out=y, residual=r), lambda: q.grouped_matmul(x, off, out=y, residual=r),  # noqa: B023
+                     lambda: fp4.w4a4_linear(M, N, K, x, d.codes, d.scales, y, residual=r)):  # noqa: B023
+            with pytest.raises(ValueError, match="share"):
+                call()
+    for y, r in good:
+        want = d.matmul(x, out_dtype=y.dtype, bias=b[0], residual=r.clone())
+        assert torch.equal(d.matmul(x, out=y, bias=b[0], residual=r), want)
+        y.zero_()
