@@ -616,7 +616,8 @@ def mx_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None
     its product contracts. With an activation, D = g f'(x w^T + bias), in g's type, takes g's place (as in the gradient of the
     activation as a layer of its own), the sum in f' being kept in float32 from the forward pass. The bias's gradient is the
     sum of g f' over the rows, from its float32 values; the residual's is g. x, w, bias and residual are float32, bfloat16 or
-    float16 on one GPU.
+    float16 on one GPU. K is 2^22 at most, and what a gradient's product contracts is too: N where x's is wanted, the rows of x where
+    w's is; more is refused.
 
     A step captured into a graph takes its gradients with torch.autograd.grad; torch's accumulation into `.grad` joins the
     stream on which an eager step that is still alive first used the leaf, which a capture cannot do."""
@@ -631,5 +632,10 @@ def mx_grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, b
     offsets: E + 1 bounds (int32 or int64) that grow from 0 or more to at most the number of rows, on the GPU: nothing waits for
     their values. Rows of no expert have no product: the result there is the residual, or zero, and so is x's gradient zero.
     An expert without rows has zero gradients. Blocks of the operands that the weights' gradients contract begin anew at
-    each expert's first row. Otherwise as mx_linear."""
+    each expert's first row. Otherwise as mx_linear.
+
+    E is 512 at most. Where x's gradient is wanted, the experts' weights are one operand along their columns, each expert's N positions
+    padded to a multiple of 256; where w's is, the rows of x and of the result's gradient are, each expert's rows padded so (8 rows write
+    32 times their codes). Such an operand has 2^22 positions at most: about 4 million rows of weights, or rows of x and 255 for
+    each expert; more is refused."""
     return _native.mx_grouped_linear(x, w, offsets, bias, activation, residual)

@@ -365,7 +365,8 @@ int fp4_dequant_mxfp4(int type, int64_t M, int64_t K, const fp4_mx* a, void* out
  * workspace and a second kernel adds the planes in order. Deterministic. A partial sum past FP32's range
  * is an infinity and stays one, or becomes NaN where two of opposite sign meet.
  * workspace: device memory, 16-byte aligned, needing no initial contents, used only while the call's kernels run
- * on `stream`; with fewer than w4a4_matmul_workspace_bytes() bytes (or NULL) K is not split. M = 0 is a no-op.
+ * on `stream`; where the planes do not fit (w4a4_matmul_workspace_bytes() bytes hold them; NULL holds none) K is not split. M = 0 is
+ * a no-op.
  * Errors: FP4_ERR_ARG (unknown type, null pointer), FP4_ERR_SHAPE, FP4_ERR_UNSUPPORTED, FP4_ERR_ALIGN, FP4_ERR_HIP.
  */
 int w4a4_matmul(int out_type, int64_t M, int64_t N, int64_t K, const fp4_mx* a, const fp4_mx* b, void* y,
